@@ -1,8 +1,9 @@
 /*
  * q3vl.h -- C ABI of libq3vl: the full-sequence causal prefill of a
  * Qwen3-VL text decoder layer and layer stack on an NVIDIA B200 (sm_100a),
- * a KV cache written by the prefill with one-token decode against it, and
- * the steps either side of the layers (embedding gather, LM head).
+ * a KV cache (bf16 or 8-bit) written by the prefill with one-token decode
+ * against it, the steps either side of the layers (embedding gather, LM
+ * head), and 8-bit rows, weights and products for serving.
  *
  * Sources of the operations (web pages, cited by title and item):
  *   [P] inferencelayer 0.2.3 src/vision.rs, `mrope_positions` -- positions
@@ -373,6 +374,144 @@ size_t q3vl_lm_head_workspace_bytes(const q3vl_config* cfg, int32_t B);
 int q3vl_lm_head(const q3vl_config* cfg, const void* x, int32_t B, const void* final_norm,
                  const void* weight, int64_t vocab, float* logits, void* ws, size_t ws_bytes,
                  q3vl_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit serving: rows, weights and the KV cache in e4m3 with block scales.
+ *
+ * The pages describe no 8-bit form; these calls exist because decode is bound
+ * by the bytes of the weights and of the cache. An 8-bit element is an OCP
+ * e4m3 byte (4 exponent bits, 3 mantissa bits, no infinity); it stands for
+ * e4m3 * 2^(u - 127), u being the E8M0 byte of its block. The scale of a
+ * block whose largest finite magnitude is A is the smallest power of two
+ * 2^s, s >= -126, with A <= 448 * 2^s (2^-126 for A = 0); elements are
+ * divided by it and rounded to nearest even. An element that is not finite is
+ * stored as NaN (0x7f) and takes no part in A. Blocks are
+ *   - 128 columns of one row (activations),
+ *   - 128 rows x 128 columns (weights),
+ *   - 128 tokens of one KV head (cache).
+ * The last block of a row or column may be shorter.
+ * ------------------------------------------------------------------------- */
+
+/* Residual add, RMSNorm and quantisation of S rows of cfg->hidden columns:
+ *   h = x + delta (rounded to cfg dtype; h = x when delta is NULL),
+ *   y = RMSNorm(h) * gain in fp32 (y = h when gain is NULL),
+ *   q, scales = the 8-bit form of y.
+ * x, delta: device [S, H] in cfg dtype; delta may be NULL.
+ * gain:     device [H] in cfg dtype, or NULL to quantise h without a norm.
+ * h:        device [S, H] out; may be x or delta. Not written when delta is
+ *           NULL (it may then be NULL).
+ * q:        device e4m3 [S, H] out, 16-byte aligned.
+ * scales:   device E8M0 [S, ceil(H / 128)] out.
+ * H <= 32768. */
+int q3vl_add_rms_norm_q8(const q3vl_config* cfg, const void* x, const void* delta, int64_t S,
+                         const void* gain, void* h, uint8_t* q, uint8_t* scales,
+                         q3vl_stream stream);
+
+/* 8-bit form of a weight matrix w [N, K] (device, cfg dtype): wq e4m3 [N, K]
+ * and ws E8M0 [ceil(N / 128), ceil(K / 128)]. K must be a multiple of 64. */
+int q3vl_quantize_weight_q8(const q3vl_config* cfg, const void* w, int64_t N, int64_t K,
+                            uint8_t* wq, uint8_t* ws, q3vl_stream stream);
+
+/* out[m][n] = sum_k x[m][k] w[n][k] (+ resid[m][n]) of 8-bit operands, summed
+ * in fp32 and rounded once to the output type.
+ * xq, xs: device e4m3 [M, K] and E8M0 [M, ceil(K / 128)] (as
+ *         q3vl_add_rms_norm_q8 writes them).
+ * wq, ws: device e4m3 [N, K] and E8M0 [ceil(N / 128), ceil(K / 128)].
+ * resid:  device [M, N] of the output type, or NULL; may be out.
+ * out:    device [M, N], bf16 or fp32 by out_dtype (enum q3vl_dtype).
+ * K must be a multiple of 64; M, N >= 1. xq, wq, resid and out 16-byte
+ * aligned. */
+int q3vl_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
+                   const uint8_t* ws, int64_t N, int64_t K, const void* resid, void* out,
+                   int32_t out_dtype, q3vl_stream stream);
+
+/* Workspace bytes of q3vl_lm_head_q8 for B rows (0 for invalid arguments). */
+size_t q3vl_lm_head_q8_workspace_bytes(const q3vl_config* cfg, int32_t B);
+
+/* q3vl_lm_head with an 8-bit output weight: the normalised rows are quantised
+ * (q3vl_add_rms_norm_q8) and multiplied by wq/ws (q3vl_linear_q8) into fp32
+ * logits. x: device bf16 [B, H], 1 <= B <= 256; wq, ws: [vocab, H] as
+ * q3vl_quantize_weight_q8 writes them. */
+int q3vl_lm_head_q8(const q3vl_config* cfg, const void* x, int32_t B, const void* final_norm,
+                    const uint8_t* wq, const uint8_t* ws, int64_t vocab, float* logits,
+                    void* wsp, size_t wsp_bytes, q3vl_stream stream);
+
+/* One layer's 8-bit cache (device memory owned by the caller). Rows are laid
+ * out as in q3vl_kv_cache with one byte per element; the scale of tokens
+ * 128 j .. 128 j + 127 of KV head g in slot s is at
+ * (s * ceil(cap / 128) + j) * nkv + g. Scales need no initial value: a block's
+ * scale is written when its first row is. */
+typedef struct q3vl_kv_cache_q8 {
+  uint8_t* k;        /* device e4m3 [n_seq][cap][nkv*hd], 16-byte aligned */
+  uint8_t* v;        /* device e4m3 [n_seq][cap][nkv*hd], 16-byte aligned */
+  uint8_t* k_scale;  /* device E8M0 [n_seq][ceil(cap/128)][nkv] */
+  uint8_t* v_scale;  /* device E8M0 [n_seq][ceil(cap/128)][nkv] */
+  int64_t cap;       /* rows per sequence slot, 1 <= cap <= 131072 */
+  int32_t n_seq;     /* sequence slots, >= 1, with n_seq * cap < 2^31 */
+} q3vl_kv_cache_q8;
+
+/* Appends K and V rows to B sequences: the rows of sequence b go to rows
+ * len[b] .. of slot seq[b]. A block that already holds earlier rows keeps the
+ * larger of its scale and the new rows'; where that grew, its earlier rows are
+ * rounded again to it. Rows behind the last appended one are left as they are.
+ * k, v:   device bf16, T rows of nkv*hd with row stride `ld` elements (a
+ *         multiple of 8): e.g. the k and v column ranges of a QKV buffer.
+ * starts: device int32 [B + 1], sequence b's rows are starts[b] ..
+ *         starts[b + 1] - 1 of the T; or NULL: T = B, one row per sequence.
+ * seq:    device int32 [B], distinct slots in [0, n_seq).
+ * len:    device int32 [B], rows already in the slot (read, not advanced).
+ * A sequence whose slot, starts or length is out of range (len[b] + rows >
+ * cap) is recorded as the device error Q3VL_ERANGE and skipped whole; starts
+ * that decrease anywhere store nothing at all. 1 <= B <= 256. bf16 configs
+ * only. */
+int q3vl_kv_store_q8(const q3vl_config* cfg, const void* k, const void* v, int64_t ld, int64_t T,
+                     const int32_t* starts, int32_t B, const q3vl_kv_cache_q8* kv,
+                     const int32_t* seq, const int32_t* len, q3vl_stream stream);
+
+/* Workspace bytes of q3vl_attention_q8 (0 for invalid arguments). */
+size_t q3vl_attention_q8_workspace_bytes(const q3vl_config* cfg, int32_t B, int64_t cap);
+
+/* Attention of one query row per sequence over the 8-bit cache: query head h
+ * of row b over rows 0 .. len[b] - 1 of KV head h / (nh/nkv) in slot seq[b],
+ * scale 1/sqrt(hd). len[b] = 0 gives a zero row.
+ * q:   device bf16 [B, nh*hd], 16-byte aligned (after the norm and MRoPE).
+ * seq: device int32 [B], slots in [0, n_seq); several rows may share one.
+ * len: device int32 [B], 0 <= len[b] <= cap. A slot or length out of range is
+ *      the device error Q3VL_ERANGE and gives a zero row.
+ * o:   device bf16 [B, nh*hd] out, 16-byte aligned.
+ * ws:  >= q3vl_attention_q8_workspace_bytes bytes, 256-byte aligned.
+ * 1 <= B <= 256, n_heads / n_kv_heads in {1, 2, 4, 8}. */
+int q3vl_attention_q8(const q3vl_config* cfg, const void* q, int32_t B,
+                      const q3vl_kv_cache_q8* kv, const int32_t* seq, const int32_t* len, void* o,
+                      void* ws, size_t ws_bytes, q3vl_stream stream);
+
+/* q3vl_layer_prefill_kv / q3vl_stack_prefill_kv with 8-bit caches: rows
+ * 0..S-1 of slot `seq` are written by q3vl_kv_store_q8's rule (the prefill's
+ * own attention reads the bf16 rows). */
+int q3vl_layer_prefill_kv_q8(const q3vl_config* cfg, const q3vl_layer* layer, void* x, int64_t S,
+                             const int32_t* pos, const void* ds_slab, const int32_t* ds_rows,
+                             int32_t n_img, const q3vl_kv_cache_q8* kv, int32_t seq, void* ws,
+                             size_t ws_bytes, q3vl_stream stream);
+int q3vl_stack_prefill_kv_q8(const q3vl_config* cfg, int32_t n_layers, const q3vl_layer* layers,
+                             const void* final_norm, void* x, int64_t S, const int32_t* pos,
+                             const void* const* ds_slabs, int32_t n_ds, const int32_t* ds_rows,
+                             int32_t n_img, const q3vl_kv_cache_q8* kv, int32_t seq, void* ws,
+                             size_t ws_bytes, q3vl_stream stream);
+
+/* Workspace bytes of the 8-bit-cache decode calls (0 for invalid arguments). */
+size_t q3vl_decode_q8_workspace_bytes(const q3vl_config* cfg, int32_t B, int64_t cap);
+
+/* q3vl_layer_decode / q3vl_stack_decode with 8-bit caches: the new token's K/V
+ * row is appended by q3vl_kv_store_q8's rule and the token attends to rows
+ * 0..len[b] as they are stored. Arguments, errors and stream order as there;
+ * ws of >= q3vl_decode_q8_workspace_bytes bytes. */
+int q3vl_layer_decode_q8(const q3vl_config* cfg, const q3vl_layer* layer, void* x, int32_t B,
+                         const int32_t* pos, const q3vl_kv_cache_q8* kv, const int32_t* seq,
+                         const int32_t* len, void* ws, size_t ws_bytes, q3vl_stream stream);
+int q3vl_stack_decode_q8(const q3vl_config* cfg, int32_t n_layers, const q3vl_layer* layers,
+                         const void* final_norm, void* x, int32_t B, const int32_t* pos,
+                         const q3vl_kv_cache_q8* kv, const int32_t* seq, const int32_t* len,
+                         void* ws, size_t ws_bytes, q3vl_stream stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics.

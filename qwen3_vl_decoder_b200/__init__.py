@@ -3,6 +3,8 @@
 The full-sequence causal prefill of a layer or a stack, a KV cache written by
 the prefill with one-token decode against it, and the steps either side: the
 token-embedding gather with the soft-token splice, and the final norm + LM head.
+For serving in 8 bits: a norm and a weight form with e4m3 outputs, their product,
+and a cache of half the bytes with the attention that reads it.
 
 A thin torch-facing binding of libq3vl's C ABI (include/q3vl.h). torch only
 provides device memory and the current stream; every step runs in the
@@ -12,12 +14,13 @@ to: without the built library, the first call raises ImportError.
 from __future__ import annotations
 
 import ctypes
-from typing import Dict, List, Optional, Sequence
+from typing import Dict, List, Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import _abi
-from ._abi import Config, KvCache as KvCacheStruct, Layer, RawWeights  # noqa: F401
+from ._abi import (Config, KvCache as KvCacheStruct, KvCacheQ8 as KvCacheQ8Struct,  # noqa: F401
+                   Layer, RawWeights)
 
 _lib_handle: Optional[ctypes.CDLL] = None
 
@@ -188,6 +191,9 @@ def stack_prefill(cfg: Config, layers: Sequence[PackedLayer], x: torch.Tensor, p
 # ---------------------------------------------------------------------------
 # KV cache and one-token decode (bf16)
 # ---------------------------------------------------------------------------
+Q8_BLOCK = 128   # columns, weight rows or tokens that share a scale
+
+
 class KvCache:
     """One layer's cache: k and v bf16 [n_seq, cap, nkv*128] on the device (K after the
     per-head norm and MRoPE, as the prefill forms it)."""
@@ -203,83 +209,147 @@ class KvCache:
         return int(self.struct.cap)
 
 
-def kv_caches(cfg: Config, n_layers: int, n_seq: int, cap: int, device="cuda") -> List[KvCache]:
-    return [KvCache(cfg, n_seq, cap, device) for _ in range(n_layers)]
+class KvCacheQ8:
+    """One layer's 8-bit cache: k and v e4m3 [n_seq, cap, nkv*128] with E8M0 scales k_scale
+    and v_scale [n_seq, ceil(cap/128), nkv], one per 128 tokens and KV head."""
+
+    def __init__(self, cfg: Config, n_seq: int, cap: int, device="cuda"):
+        dkv = cfg.n_kv_heads * cfg.head_dim
+        blocks = -(-cap // Q8_BLOCK)
+
+        def zeros(*shape):
+            return torch.zeros(shape, dtype=torch.uint8, device=device)
+
+        self._set(cfg, zeros(n_seq, cap, dkv).view(torch.float8_e4m3fn),
+                  zeros(n_seq, cap, dkv).view(torch.float8_e4m3fn),
+                  zeros(n_seq, blocks, cfg.n_kv_heads).view(torch.float8_e8m0fnu),
+                  zeros(n_seq, blocks, cfg.n_kv_heads).view(torch.float8_e8m0fnu))
+
+    @classmethod
+    def of(cls, cfg: Config, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+           v_scale: torch.Tensor) -> "KvCacheQ8":
+        """A cache over tensors that the caller holds already (kept, not copied)."""
+        kv = cls.__new__(cls)
+        kv._set(cfg, k, v, k_scale, v_scale)
+        return kv
+
+    def _set(self, cfg, k, v, k_scale, v_scale):
+        n_seq, cap, dkv = k.shape
+        blocks = -(-cap // Q8_BLOCK)
+        for t, name in ((k, "k"), (v, "v")):
+            _arg(t, name, (torch.float8_e4m3fn,), (n_seq, cap, cfg.n_kv_heads * cfg.head_dim),
+                 k.device)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _arg(t, name, (torch.float8_e8m0fnu,), (n_seq, blocks, cfg.n_kv_heads), k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.struct = KvCacheQ8Struct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                      v_scale.data_ptr(), cap, n_seq)
+
+    @property
+    def cap(self) -> int:
+        return int(self.struct.cap)
 
 
-def _kv_array(kvs: Sequence[KvCache]):
-    return (KvCacheStruct * len(kvs))(*[kv.struct for kv in kvs])
+def kv_caches(cfg: Config, n_layers: int, n_seq: int, cap: int, device="cuda",
+              dtype="bf16") -> List[Union[KvCache, "KvCacheQ8"]]:
+    """Caches of n_layers layers; dtype "bf16", or "fp8" for KvCacheQ8."""
+    if dtype not in ("bf16", "fp8"):
+        raise Q3VLError(_abi.EUNSUPPORTED, f"cache dtype must be 'bf16' or 'fp8', not {dtype!r}")
+    cls = KvCache if dtype == "bf16" else KvCacheQ8
+    return [cls(cfg, n_seq, cap, device) for _ in range(n_layers)]
+
+
+def _is_q8(kvs: Sequence[Union[KvCache, KvCacheQ8]]) -> bool:
+    """Whether the layers' caches are 8-bit; all of them have to be of one kind."""
+    q8 = [isinstance(kv, KvCacheQ8) for kv in kvs]
+    if any(q8) and not all(q8):
+        raise Q3VLError(_abi.EINVAL, "the layers' caches must be all bf16 or all 8-bit")
+    return any(q8)
+
+
+def _kv_array(kvs: Sequence[Union[KvCache, KvCacheQ8]]):
+    struct = KvCacheQ8Struct if _is_q8(kvs) else KvCacheStruct
+    return (struct * len(kvs))(*[kv.struct for kv in kvs])
 
 
 def layer_prefill_kv(cfg: Config, layer: PackedLayer, x: torch.Tensor, pos: torch.Tensor,
-                     kv: KvCache, seq: int = 0, ds_slab: Optional[torch.Tensor] = None,
+                     kv: Union[KvCache, KvCacheQ8], seq: int = 0, ds_slab: Optional[torch.Tensor] = None,
                      ds_rows: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
-    """layer_prefill that also writes rows 0..S-1 of cache slot `seq`."""
+    """layer_prefill that also writes rows 0..S-1 of cache slot `seq` (bf16 or 8-bit)."""
     S = x.shape[0]
     ws = workspace(cfg, S, x.device) if ws is None else ws
     n_img = 0 if ds_rows is None else ds_rows.numel()
-    _check(lib().q3vl_layer_prefill_kv(ctypes.byref(cfg), ctypes.byref(layer.views), _ptr(x), S,
-                                      _ptr(pos), _ptr(ds_slab), _ptr(ds_rows), n_img,
-                                      ctypes.byref(kv.struct), seq, _ptr(ws), ws.numel(),
-                                      _stream(stream)))
+    fn = lib().q3vl_layer_prefill_kv_q8 if _is_q8([kv]) else lib().q3vl_layer_prefill_kv
+    _check(fn(ctypes.byref(cfg), ctypes.byref(layer.views), _ptr(x), S, _ptr(pos), _ptr(ds_slab),
+              _ptr(ds_rows), n_img, ctypes.byref(kv.struct), seq, _ptr(ws), ws.numel(),
+              _stream(stream)))
     return x
 
 
 def stack_prefill_kv(cfg: Config, layers: Sequence[PackedLayer], x: torch.Tensor,
-                     pos: torch.Tensor, kvs: Sequence[KvCache], seq: int = 0,
+                     pos: torch.Tensor, kvs: Sequence[Union[KvCache, KvCacheQ8]], seq: int = 0,
                      final_norm: Optional[torch.Tensor] = None,
                      ds_slabs: Sequence[torch.Tensor] = (), ds_rows: Optional[torch.Tensor] = None,
                      ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """stack_prefill that also writes each layer's rows 0..S-1 of cache slot `seq`."""
+    """stack_prefill that also writes each layer's rows 0..S-1 of cache slot `seq` (caches all
+    bf16 or all 8-bit)."""
     S = x.shape[0]
     ws = workspace(cfg, S, x.device) if ws is None else ws
     arr = (Layer * len(layers))(*[l.views for l in layers])
     slabs = (ctypes.c_void_p * max(1, len(ds_slabs)))(*[s.data_ptr() for s in ds_slabs])
     n_img = 0 if ds_rows is None else ds_rows.numel()
-    _check(lib().q3vl_stack_prefill_kv(ctypes.byref(cfg), len(layers), arr, _ptr(final_norm),
-                                      _ptr(x), S, _ptr(pos), slabs if ds_slabs else None,
-                                      len(ds_slabs), _ptr(ds_rows), n_img, _kv_array(kvs), seq,
-                                      _ptr(ws), ws.numel(), _stream(stream)))
+    fn = lib().q3vl_stack_prefill_kv_q8 if _is_q8(kvs) else lib().q3vl_stack_prefill_kv
+    _check(fn(ctypes.byref(cfg), len(layers), arr, _ptr(final_norm), _ptr(x), S, _ptr(pos),
+              slabs if ds_slabs else None, len(ds_slabs), _ptr(ds_rows), n_img, _kv_array(kvs),
+              seq, _ptr(ws), ws.numel(), _stream(stream)))
     return x
 
 
-def decode_workspace_bytes(cfg: Config, B: int, cap: int) -> int:
-    return int(lib().q3vl_decode_workspace_bytes(ctypes.byref(cfg), B, cap))
+def decode_workspace_bytes(cfg: Config, B: int, cap: int, dtype="bf16") -> int:
+    """dtype: the caches' ("bf16" or "fp8")."""
+    fn = lib().q3vl_decode_workspace_bytes if dtype == "bf16" else \
+        lib().q3vl_decode_q8_workspace_bytes
+    return int(fn(ctypes.byref(cfg), B, cap))
 
 
-def decode_workspace(cfg: Config, B: int, cap: int, device="cuda") -> torch.Tensor:
-    n = decode_workspace_bytes(cfg, B, cap)
+def decode_workspace(cfg: Config, B: int, cap: int, device="cuda", dtype="bf16") -> torch.Tensor:
+    n = decode_workspace_bytes(cfg, B, cap, dtype)
     if n == 0:
         _check(_abi.EINVAL)
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def layer_decode(cfg: Config, layer: PackedLayer, x: torch.Tensor, pos: torch.Tensor,
-                 kv: KvCache, seq: torch.Tensor, lens: torch.Tensor,
+                 kv: Union[KvCache, KvCacheQ8], seq: torch.Tensor, lens: torch.Tensor,
                  ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """One new token per sequence (x [B, H] in place): token b's K/V go to row lens[b] of
     slot seq[b], and it attends to rows 0..lens[b] of that slot."""
     B = x.shape[0]
-    ws = decode_workspace(cfg, B, kv.cap, x.device) if ws is None else ws
-    _check(lib().q3vl_layer_decode(ctypes.byref(cfg), ctypes.byref(layer.views), _ptr(x), B,
-                                  _ptr(pos), ctypes.byref(kv.struct), _ptr(seq), _ptr(lens),
-                                  _ptr(ws), ws.numel(), _stream(stream)))
+    q8 = _is_q8([kv])
+    if ws is None:
+        ws = decode_workspace(cfg, B, kv.cap, x.device, "fp8" if q8 else "bf16")
+    fn = lib().q3vl_layer_decode_q8 if q8 else lib().q3vl_layer_decode
+    _check(fn(ctypes.byref(cfg), ctypes.byref(layer.views), _ptr(x), B, _ptr(pos),
+              ctypes.byref(kv.struct), _ptr(seq), _ptr(lens), _ptr(ws), ws.numel(),
+              _stream(stream)))
     return x
 
 
 def stack_decode(cfg: Config, layers: Sequence[PackedLayer], x: torch.Tensor, pos: torch.Tensor,
-                 kvs: Sequence[KvCache], seq: torch.Tensor, lens: torch.Tensor,
+                 kvs: Sequence[Union[KvCache, KvCacheQ8]], seq: torch.Tensor, lens: torch.Tensor,
                  final_norm: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
     """layer_decode through every layer, then the optional final norm; x in place."""
     B = x.shape[0]
     cap = max(kv.cap for kv in kvs)
-    ws = decode_workspace(cfg, B, cap, x.device) if ws is None else ws
+    q8 = _is_q8(kvs)
+    if ws is None:
+        ws = decode_workspace(cfg, B, cap, x.device, "fp8" if q8 else "bf16")
     arr = (Layer * len(layers))(*[l.views for l in layers])
-    _check(lib().q3vl_stack_decode(ctypes.byref(cfg), len(layers), arr, _ptr(final_norm), _ptr(x),
-                                  B, _ptr(pos), _kv_array(kvs), _ptr(seq), _ptr(lens), _ptr(ws),
-                                  ws.numel(), _stream(stream)))
+    fn = lib().q3vl_stack_decode_q8 if q8 else lib().q3vl_stack_decode
+    _check(fn(ctypes.byref(cfg), len(layers), arr, _ptr(final_norm), _ptr(x), B, _ptr(pos),
+              _kv_array(kvs), _ptr(seq), _ptr(lens), _ptr(ws), ws.numel(), _stream(stream)))
     return x
 
 
@@ -306,9 +376,12 @@ def embed(cfg: Config, table: torch.Tensor, tokens: torch.Tensor,
 
 
 def lm_head(cfg: Config, x_rows: torch.Tensor, final_norm: Optional[torch.Tensor],
-            weight: torch.Tensor, logits: Optional[torch.Tensor] = None,
+            weight: Union[torch.Tensor, "LinearQ8"], logits: Optional[torch.Tensor] = None,
             ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """logits [B, vocab] fp32 = RMSNorm(x_rows, final_norm) weight^T (weight: [vocab, H])."""
+    """logits [B, vocab] fp32 = RMSNorm(x_rows, final_norm) weight^T (weight: [vocab, H], bf16
+    or its 8-bit form, with which the normalised rows are quantised too)."""
+    if isinstance(weight, LinearQ8):
+        return _lm_head_q8(cfg, x_rows, final_norm, weight, logits, ws, stream)
     B, vocab = x_rows.shape[0], weight.shape[0]
     if logits is None:
         logits = torch.empty((B, vocab), dtype=torch.float32, device=x_rows.device)
@@ -320,6 +393,245 @@ def lm_head(cfg: Config, x_rows: torch.Tensor, final_norm: Optional[torch.Tensor
     _check(lib().q3vl_lm_head(ctypes.byref(cfg), _ptr(x_rows), B, _ptr(final_norm), _ptr(weight),
                              vocab, _ptr(logits), _ptr(ws), ws.numel(), _stream(stream)))
     return logits
+
+
+# ---------------------------------------------------------------------------
+# 8-bit serving: e4m3 rows, weights and cache with power-of-two block scales
+# ---------------------------------------------------------------------------
+_ROW_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _arg(t: torch.Tensor, name: str, dtypes, shape=None, device=None) -> None:
+    """Raises unless t is a contiguous tensor of one of `dtypes` (and the shape and device)."""
+    if not isinstance(t, torch.Tensor):
+        raise Q3VLError(_abi.EINVAL, f"{name} must be a tensor")
+    if t.dtype not in dtypes:
+        raise Q3VLError(_abi.EINVAL, f"{name} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise Q3VLError(_abi.EINVAL, f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise Q3VLError(_abi.EINVAL, f"{name} is on {t.device}, not {device}")
+    if not t.is_contiguous():
+        raise Q3VLError(_abi.EINVAL, f"{name} must be contiguous")
+
+
+class _on:
+    """Makes a tensor's device current for a call (the library works on the current one), and
+    the caller's stream if one is given, so that what the call allocates belongs to that stream;
+    gives the stream to launch on."""
+
+    def __init__(self, t: torch.Tensor, stream=None):
+        if t.device.type != "cuda":
+            raise Q3VLError(_abi.EINVAL, f"tensors must be on a CUDA device, not {t.device}")
+        if stream is not None and stream.device != t.device:
+            raise Q3VLError(_abi.EINVAL, f"the stream is on {stream.device}, tensors on {t.device}")
+        self.device, self.stream, self.guards = t.device, stream, []
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(self.device))
+        if self.stream is not None:
+            self.guards.append(torch.cuda.stream(self.stream))
+        for guard in self.guards:
+            guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        for guard in reversed(self.guards):
+            guard.__exit__(*exc)
+
+
+class LinearQ8:
+    """An 8-bit weight: e4m3 [N, K] with E8M0 scales [ceil(N/128), ceil(K/128)]."""
+
+    def __init__(self, weight: torch.Tensor, scales: torch.Tensor):
+        _arg(weight, "weight", (torch.float8_e4m3fn,))
+        if weight.dim() != 2:
+            raise Q3VLError(_abi.EINVAL, f"weight must be [N, K], not {tuple(weight.shape)}")
+        N, K = weight.shape
+        _arg(scales, "scales", (torch.float8_e8m0fnu,), (-(-N // Q8_BLOCK), -(-K // Q8_BLOCK)),
+             weight.device)
+        self.weight, self.scales = weight, scales
+
+    @property
+    def shape(self) -> Tuple[int, int]:
+        return tuple(self.weight.shape)
+
+
+def quantize_weight_q8(w: torch.Tensor, stream=None) -> LinearQ8:
+    """The 8-bit form of a weight [N, K] (bf16 or fp32), one scale per 128 x 128 block."""
+    _arg(w, "w", _ROW_TYPES)
+    if w.dim() != 2:
+        raise Q3VLError(_abi.EINVAL, f"w must be [N, K], not {tuple(w.shape)}")
+    N, K = w.shape
+    cfg = config(128, 1, 1, 128, "bf16" if w.dtype == torch.bfloat16 else "fp32")
+    with _on(w, stream) as st:
+        wq = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=w.device)
+        ws = torch.empty((-(-N // Q8_BLOCK), -(-K // Q8_BLOCK)), dtype=torch.float8_e8m0fnu,
+                         device=w.device)
+        _check(lib().q3vl_quantize_weight_q8(ctypes.byref(cfg), _ptr(w), N, K, _ptr(wq), _ptr(ws),
+                                             st))
+    return LinearQ8(wq, ws)
+
+
+def add_rms_norm_q8(cfg: Config, x: torch.Tensor, gain: Optional[torch.Tensor],
+                    delta: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(h, q, scales): h = x + delta (x itself without a delta), and the 8-bit form of
+    RMSNorm(h) * gain: e4m3 [S, H] with E8M0 scales [S, ceil(H/128)].
+
+    gain None quantises h without a norm. h: where to write the sum (x for in place); a new
+    tensor by default.
+    """
+    dt = (torch_dtype(cfg),)
+    _arg(x, "x", dt)
+    if x.dim() != 2 or x.shape[1] != cfg.hidden:
+        raise Q3VLError(_abi.EINVAL, f"x must be [S, {cfg.hidden}], not {tuple(x.shape)}")
+    S, H = x.shape
+    if gain is not None:
+        _arg(gain, "gain", dt, (H,), x.device)
+    if delta is None:
+        if h is not None and h is not x:
+            raise Q3VLError(_abi.EINVAL, "without a delta, h is x")
+        h = x
+    else:
+        _arg(delta, "delta", dt, (S, H), x.device)
+        if h is not None:
+            _arg(h, "h", dt, (S, H), x.device)
+    with _on(x, stream) as st:
+        if h is None:
+            h = torch.empty_like(x)
+        q = torch.empty((S, H), dtype=torch.float8_e4m3fn, device=x.device)
+        sc = torch.empty((S, -(-H // Q8_BLOCK)), dtype=torch.float8_e8m0fnu, device=x.device)
+        _check(lib().q3vl_add_rms_norm_q8(ctypes.byref(cfg), _ptr(x), _ptr(delta), S, _ptr(gain),
+                                          _ptr(h), _ptr(q), _ptr(sc), st))
+    return h, q, sc
+
+
+def linear_q8(xq: torch.Tensor, scales: torch.Tensor, lin: LinearQ8,
+              resid: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """[M, N] = x W^T (+ resid) of 8-bit rows (as add_rms_norm_q8 gives them) and an 8-bit
+    weight, summed in fp32 and rounded once to out_dtype (bfloat16 or float32)."""
+    _arg(xq, "xq", (torch.float8_e4m3fn,))
+    N, K = lin.weight.shape
+    if xq.dim() != 2 or xq.shape[1] != K:
+        raise Q3VLError(_abi.EINVAL, f"xq must be [M, {K}], not {tuple(xq.shape)}")
+    M = xq.shape[0]
+    _arg(scales, "scales", (torch.float8_e8m0fnu,), (M, -(-K // Q8_BLOCK)), xq.device)
+    if lin.weight.device != xq.device:
+        raise Q3VLError(_abi.EINVAL, f"the weight is on {lin.weight.device}, xq on {xq.device}")
+    if out_dtype not in _ROW_TYPES:
+        raise Q3VLError(_abi.EUNSUPPORTED, f"out_dtype must be bfloat16 or float32, not {out_dtype}")
+    if resid is not None:
+        _arg(resid, "resid", (out_dtype,), (M, N), xq.device)
+    if out is not None:
+        _arg(out, "out", (out_dtype,), (M, N), xq.device)
+    with _on(xq, stream) as st:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=xq.device)
+        _check(lib().q3vl_linear_q8(
+            _ptr(xq), _ptr(scales), M, _ptr(lin.weight), _ptr(lin.scales), N, K, _ptr(resid),
+            _ptr(out), _abi.DTYPE_BF16 if out_dtype == torch.bfloat16 else _abi.DTYPE_FP32, st))
+    return out
+
+
+def _lm_head_q8(cfg, x_rows, final_norm, lin, logits, ws, stream):
+    _arg(x_rows, "x_rows", (torch.bfloat16,))
+    B, (vocab, K) = x_rows.shape[0], lin.shape
+    if x_rows.dim() != 2 or x_rows.shape[1] != cfg.hidden or K != cfg.hidden:
+        raise Q3VLError(_abi.EINVAL, f"x_rows and weight must have {cfg.hidden} columns")
+    if final_norm is not None:
+        _arg(final_norm, "final_norm", (torch.bfloat16,), (cfg.hidden,), x_rows.device)
+    if lin.weight.device != x_rows.device:
+        raise Q3VLError(_abi.EINVAL, f"the weight is on {lin.weight.device}, x_rows on {x_rows.device}")
+    if logits is not None:
+        _arg(logits, "logits", (torch.float32,), (B, vocab), x_rows.device)
+    with _on(x_rows, stream) as st:
+        if logits is None:
+            logits = torch.empty((B, vocab), dtype=torch.float32, device=x_rows.device)
+        if ws is None:
+            n = int(lib().q3vl_lm_head_q8_workspace_bytes(ctypes.byref(cfg), B))
+            if n == 0:
+                _check(_abi.EINVAL)
+            ws = torch.empty(n, dtype=torch.uint8, device=x_rows.device)
+        _check(lib().q3vl_lm_head_q8(ctypes.byref(cfg), _ptr(x_rows), B, _ptr(final_norm),
+                                     _ptr(lin.weight), _ptr(lin.scales), vocab, _ptr(logits),
+                                     _ptr(ws), ws.numel(), st))
+    return logits
+
+
+def _index(t: torch.Tensor, name: str, n: int, device) -> None:
+    _arg(t, name, (torch.int32,), (n,), device)
+
+
+def kv_store_q8(cfg: Config, k: torch.Tensor, v: torch.Tensor, kv: KvCacheQ8, seq: torch.Tensor,
+                lens: torch.Tensor, starts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Appends rows to sequences of an 8-bit cache: rows starts[b]..starts[b+1]-1 of k and v go to
+    rows lens[b].. of slot seq[b] (without starts, row b alone).
+
+    k, v: bf16 [T, nkv*128] with contiguous rows and one row stride, such as the k and v column
+    ranges of a QKV buffer. seq (distinct slots) and lens: int32 [B]; starts: int32 [B+1]. lens
+    is not advanced.
+    """
+    dkv = cfg.n_kv_heads * cfg.head_dim
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != dkv:
+            raise Q3VLError(_abi.EINVAL, f"{name} must be bfloat16 [T, {dkv}], not "
+                                         f"{t.dtype} {tuple(t.shape)}")
+        if t.shape[0] > 0 and (t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < dkv)):
+            raise Q3VLError(_abi.EINVAL, f"{name} must have contiguous rows that do not overlap")
+        if t.device != kv.k.device:
+            raise Q3VLError(_abi.EINVAL, f"{name} is on {t.device}, the cache on {kv.k.device}")
+    T, B = k.shape[0], seq.numel()
+    if v.shape != k.shape or (T > 1 and v.stride(0) != k.stride(0)):
+        raise Q3VLError(_abi.EINVAL, "k and v must have one shape and row stride")
+    if kv.k.shape[2] != dkv:
+        raise Q3VLError(_abi.EINVAL, f"the cache has rows of {kv.k.shape[2]}, the config {dkv}")
+    _index(seq, "seq", B, k.device)
+    _index(lens, "lens", B, k.device)
+    if starts is not None:
+        _index(starts, "starts", B + 1, k.device)
+    ld = k.stride(0) if T > 1 else dkv
+    with _on(k, stream) as st:
+        _check(lib().q3vl_kv_store_q8(ctypes.byref(cfg), _ptr(k), _ptr(v), ld, T, _ptr(starts), B,
+                                      ctypes.byref(kv.struct), _ptr(seq), _ptr(lens), st))
+
+
+def attention_q8_workspace(cfg: Config, B: int, cap: int, device="cuda") -> torch.Tensor:
+    n = int(lib().q3vl_attention_q8_workspace_bytes(ctypes.byref(cfg), B, cap))
+    if n == 0:
+        _check(_abi.EINVAL)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def attention_q8(cfg: Config, q: torch.Tensor, kv: KvCacheQ8, seq: torch.Tensor,
+                 lens: torch.Tensor, o: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """o [B, nh*128] bf16: the attention of query row b (q [B, nh*128] bf16) over rows
+    0..lens[b]-1 of slot seq[b] of an 8-bit cache; a length of 0 gives a zero row."""
+    dq = cfg.n_heads * cfg.head_dim
+    _arg(q, "q", (torch.bfloat16,))
+    if q.dim() != 2 or q.shape[1] != dq:
+        raise Q3VLError(_abi.EINVAL, f"q must be [B, {dq}], not {tuple(q.shape)}")
+    if kv.k.shape[2] != cfg.n_kv_heads * cfg.head_dim:
+        raise Q3VLError(_abi.EINVAL, f"the cache has rows of {kv.k.shape[2]}, the config "
+                                     f"{cfg.n_kv_heads * cfg.head_dim}")
+    if kv.k.device != q.device:
+        raise Q3VLError(_abi.EINVAL, f"the cache is on {kv.k.device}, q on {q.device}")
+    B = q.shape[0]
+    _index(seq, "seq", B, q.device)
+    _index(lens, "lens", B, q.device)
+    if o is not None:
+        _arg(o, "o", (torch.bfloat16,), (B, dq), q.device)
+    with _on(q, stream) as st:
+        if o is None:
+            o = torch.empty_like(q)
+        if ws is None:
+            ws = attention_q8_workspace(cfg, B, kv.cap, q.device)
+        _check(lib().q3vl_attention_q8(ctypes.byref(cfg), _ptr(q), B, ctypes.byref(kv.struct),
+                                       _ptr(seq), _ptr(lens), _ptr(o), _ptr(ws), ws.numel(), st))
+    return o
 
 
 # ---------------------------------------------------------------------------

@@ -46,6 +46,11 @@ class KvCache(ctypes.Structure):
                 ("n_seq", ctypes.c_int32)]
 
 
+class KvCacheQ8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("cap", ctypes.c_int64), ("n_seq", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -91,6 +96,27 @@ SIGNATURES = {
     "q3vl_embed": (ctypes.c_int, [_CFG, _P, _I64, _P, _I64, _P, _P, _I32, _P, _P, _SZ, _P]),
     "q3vl_lm_head_workspace_bytes": (_SZ, [_CFG, _I32]),
     "q3vl_lm_head": (ctypes.c_int, [_CFG, _P, _I32, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "q3vl_add_rms_norm_q8": (ctypes.c_int, [_CFG, _P, _P, _I64, _P, _P, _P, _P, _P]),
+    "q3vl_quantize_weight_q8": (ctypes.c_int, [_CFG, _P, _I64, _I64, _P, _P, _P]),
+    "q3vl_linear_q8": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I32, _P]),
+    "q3vl_lm_head_q8_workspace_bytes": (_SZ, [_CFG, _I32]),
+    "q3vl_lm_head_q8": (ctypes.c_int, [_CFG, _P, _I32, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "q3vl_kv_store_q8": (ctypes.c_int, [_CFG, _P, _P, _I64, _I64, _P, _I32,
+                                        ctypes.POINTER(KvCacheQ8), _P, _P, _P]),
+    "q3vl_attention_q8_workspace_bytes": (_SZ, [_CFG, _I32, _I64]),
+    "q3vl_attention_q8": (ctypes.c_int, [_CFG, _P, _I32, ctypes.POINTER(KvCacheQ8), _P, _P, _P,
+                                         _P, _SZ, _P]),
+    "q3vl_layer_prefill_kv_q8": (ctypes.c_int, [_CFG, ctypes.POINTER(Layer), _P, _I64, _P, _P, _P,
+                                                _I32, ctypes.POINTER(KvCacheQ8), _I32, _P, _SZ,
+                                                _P]),
+    "q3vl_stack_prefill_kv_q8": (ctypes.c_int, [_CFG, _I32, ctypes.POINTER(Layer), _P, _P, _I64,
+                                                _P, ctypes.POINTER(_P), _I32, _P, _I32,
+                                                ctypes.POINTER(KvCacheQ8), _I32, _P, _SZ, _P]),
+    "q3vl_decode_q8_workspace_bytes": (_SZ, [_CFG, _I32, _I64]),
+    "q3vl_layer_decode_q8": (ctypes.c_int, [_CFG, ctypes.POINTER(Layer), _P, _I32, _P,
+                                            ctypes.POINTER(KvCacheQ8), _P, _P, _P, _SZ, _P]),
+    "q3vl_stack_decode_q8": (ctypes.c_int, [_CFG, _I32, ctypes.POINTER(Layer), _P, _P, _I32, _P,
+                                            ctypes.POINTER(KvCacheQ8), _P, _P, _P, _SZ, _P]),
     "q3vl_device_status": (ctypes.c_int, [_P, ctypes.POINTER(_I32), ctypes.POINTER(_I32)]),
     "q3vl_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint32, _P]),
     "q3vl_set_stage_events": (ctypes.c_int, [ctypes.POINTER(_P), _I32]),

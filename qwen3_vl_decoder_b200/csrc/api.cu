@@ -3,6 +3,7 @@
 // on the caller's stream; nothing here synchronises except
 // q3vl_device_status().
 #include <atomic>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <string>
@@ -390,12 +391,13 @@ int run_down(const q3vl_config& c, const q3vl_layer& w, const void* act, const v
 // x in the workspace, so P2 is skipped; `leave_x_stats`: this layer's down
 // epilogue leaves them for the next layer (bf16 path only). `inv1_ready`:
 // the layer prologue already wrote P2's inv_rms.
-// `kv` (optional): the K/V rows of this layer are also written into rows
-// 0..S-1 of slot `kv_seq` of that cache.
+// `kv` or `kv8` (optional): the K/V rows of this layer are also written into
+// rows 0..S-1 of slot `kv_seq` of that bf16 or 8-bit cache.
 int run_layer(const q3vl_config& c, const q3vl_layer& w, void* x, int64_t S, char* ws,
               const WsLayout& L, const void* ds_slab, cudaStream_t st, bool x_stats_ready = false,
               bool leave_x_stats = false, const q3vl_kv_cache* kv = nullptr,
-              int32_t kv_seq = 0, bool inv1_ready = false) {
+              int32_t kv_seq = 0, bool inv1_ready = false,
+              const q3vl_kv_cache_q8* kv8 = nullptr) {
   float* cs = reinterpret_cast<float*>(ws + L.cos_sin);
   float* inv1 = reinterpret_cast<float*>(ws + L.inv1);
   float* inv2 = reinterpret_cast<float*>(ws + L.inv2);
@@ -412,6 +414,12 @@ int run_layer(const q3vl_config& c, const q3vl_layer& w, void* x, int64_t S, cha
   stage_event(2, st);
   Q3VL_TRY(run_qkv(c, w, x, S, inv1, cs, qkv, sk, st, use_x_stats ? rowsq_x : nullptr));
   if (kv != nullptr) Q3VL_CUDA(launch_kv_store(c, qkv, S, *kv, kv_seq, st), "kv cache store");
+  if (kv8 != nullptr) {
+    const char* k = static_cast<const char*>(qkv) + q_dim(c) * 2;
+    Q3VL_CUDA(launch_kv_store_q8(c, k, k + kv_dim(c) * 2, qkv_dim(c), S, nullptr, 1, *kv8, nullptr,
+                                 nullptr, kv_seq, st),
+              "8-bit kv cache store");
+  }
   stage_event(3, st);
   Q3VL_TRY(run_attention(c, qkv, S, o, st));
   stage_event(4, st);
@@ -477,18 +485,31 @@ int step_sk(const q3vl_config& c, int64_t S, void* ws, size_t ws_bytes, cudaStre
   return clear_sk_flags(*out, st);
 }
 
+int check_kv_size(int64_t cap, int32_t n_seq) {
+  if (cap < 1 || n_seq < 1)
+    return set_error(Q3VL_EINVAL, "kv cache needs cap >= 1 and n_seq >= 1");
+  if (cap > 131072)
+    return set_error(Q3VL_EUNSUPPORTED, "kv cache cap above 131072 rows per slot");
+  if (int64_t(n_seq) * cap > int64_t(0x7fffffff))
+    return set_error(Q3VL_EINVAL, "kv cache n_seq * cap must stay below 2^31 rows");
+  return Q3VL_OK;
+}
+
 int check_kv(const q3vl_config& c, const q3vl_kv_cache* kv, const char* what) {
   if (kv == nullptr) return set_error(Q3VL_EINVAL, std::string(what) + " is NULL");
   Q3VL_TRY(check_ptr(kv->k, "kv cache k"));
   Q3VL_TRY(check_ptr(kv->v, "kv cache v"));
-  if (kv->cap < 1 || kv->n_seq < 1)
-    return set_error(Q3VL_EINVAL, "kv cache needs cap >= 1 and n_seq >= 1");
-  if (kv->cap > 131072)
-    return set_error(Q3VL_EUNSUPPORTED, "kv cache cap above 131072 rows per slot");
-  if (int64_t(kv->n_seq) * kv->cap > int64_t(0x7fffffff))
-    return set_error(Q3VL_EINVAL, "kv cache n_seq * cap must stay below 2^31 rows");
   (void)c;
-  return Q3VL_OK;
+  return check_kv_size(kv->cap, kv->n_seq);
+}
+
+int check_kv_q8(const q3vl_kv_cache_q8* kv, const char* what) {
+  if (kv == nullptr) return set_error(Q3VL_EINVAL, std::string(what) + " is NULL");
+  Q3VL_TRY(check_ptr(kv->k, "kv cache k"));
+  Q3VL_TRY(check_ptr(kv->v, "kv cache v"));
+  Q3VL_TRY(check_ptr(kv->k_scale, "kv cache k_scale", false));
+  Q3VL_TRY(check_ptr(kv->v_scale, "kv cache v_scale", false));
+  return check_kv_size(kv->cap, kv->n_seq);
 }
 
 // The decode path covers bf16 layers whose query-group size is 1, 2, 4 or 8
@@ -519,12 +540,40 @@ int check_dec_ws(const q3vl_config& c, int32_t B, int64_t cap, const void* ws, s
   return Q3VL_OK;
 }
 
+// The workspace of a decode over 8-bit caches: the decode regions, then this
+// token's bf16 K and V rows [B][nkv*hd] (a one-row cache per token for the QKV
+// projection: slot iota[b], row zero[b]) and the attention's partials.
+struct DecQ8Layout {
+  DecLayout d;
+  size_t k_new = 0, v_new = 0, iota = 0, zero = 0, att = 0, total = 0;
+};
+
+DecQ8Layout dec_q8_layout(const q3vl_config& c, int B, int64_t cap) {
+  DecQ8Layout L;
+  L.d = dec_layout(c, B, 1);
+  size_t off = L.d.total;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  L.k_new = take(size_t(B) * kv_dim(c) * 2);
+  L.v_new = take(size_t(B) * kv_dim(c) * 2);
+  L.iota = take(size_t(B) * sizeof(int32_t));
+  L.zero = take(size_t(B) * sizeof(int32_t));
+  L.att = take(attention_q8_ws_bytes(c, B, cap));
+  L.total = off;
+  return L;
+}
+
 // One layer of the decode on a prepared workspace (cos/sin of the B new
 // positions written, tickets zero). `x_stats_ready`: the previous layer's
-// down epilogue left the row sums of squares of x.
+// down epilogue left the row sums of squares of x. Exactly one of `kv` and
+// `kv8` is given; `L8` is the layout of an 8-bit-cache decode.
 int run_decode_layer(const q3vl_config& c, const q3vl_layer& w, void* x, int32_t B,
-                     const q3vl_kv_cache& kv, const int32_t* seq, const int32_t* len, char* ws,
-                     const DecLayout& L, cudaStream_t st, bool x_stats_ready, bool leave_x_stats) {
+                     const q3vl_kv_cache* kv, const int32_t* seq, const int32_t* len, char* ws,
+                     const DecLayout& L, cudaStream_t st, bool x_stats_ready, bool leave_x_stats,
+                     const q3vl_kv_cache_q8* kv8 = nullptr, const DecQ8Layout* L8 = nullptr) {
   const int64_t H = c.hidden, I = c.intermediate, Dq = q_dim(c);
   float* inv = reinterpret_cast<float*>(ws + L.inv);
   float* rowsq_h = reinterpret_cast<float*>(ws + L.rowsq_h);
@@ -545,13 +594,26 @@ int run_decode_layer(const q3vl_config& c, const q3vl_layer& w, void* x, int32_t
   a.rowsq_n = static_cast<int>(H / 128); a.rowsq_width = static_cast<float>(H);
   a.bias = w.b_qkv; a.q_norm = w.q_norm; a.k_norm = w.k_norm;
   a.cos_sin = reinterpret_cast<const float*>(ws + L.cos_sin);
-  a.k_cache = kv.k; a.v_cache = kv.v; a.cap = kv.cap; a.n_seq = kv.n_seq; a.seq = seq; a.len = len;
-  Q3VL_CUDA(launch_decode_gemm(Epi::kQkv, a, st), "decode qkv projection");
-  // P5 over the cache
-  Q3VL_CUDA(launch_decode_attention(c, q, kv, seq, len, B, o,
-                                    reinterpret_cast<float*>(ws + L.att_part),
-                                    reinterpret_cast<uint32_t*>(ws + L.att_tickets), st),
-            "decode attention");
+  if (kv8 == nullptr) {
+    a.k_cache = kv->k; a.v_cache = kv->v; a.cap = kv->cap; a.n_seq = kv->n_seq;
+    a.seq = seq; a.len = len;
+    Q3VL_CUDA(launch_decode_gemm(Epi::kQkv, a, st), "decode qkv projection");
+    // P5 over the cache
+    Q3VL_CUDA(launch_decode_attention(c, q, *kv, seq, len, B, o,
+                                      reinterpret_cast<float*>(ws + L.att_part),
+                                      reinterpret_cast<uint32_t*>(ws + L.att_tickets), st),
+              "decode attention");
+  } else {
+    a.k_cache = ws + L8->k_new; a.v_cache = ws + L8->v_new; a.cap = 1; a.n_seq = B;
+    a.seq = reinterpret_cast<const int32_t*>(ws + L8->iota);
+    a.len = reinterpret_cast<const int32_t*>(ws + L8->zero);
+    Q3VL_CUDA(launch_decode_gemm(Epi::kQkv, a, st), "decode qkv projection");
+    Q3VL_CUDA(launch_kv_store_q8(c, ws + L8->k_new, ws + L8->v_new, kv_dim(c), B, nullptr, B, *kv8,
+                                 seq, len, 0, st),
+              "8-bit kv cache store");
+    Q3VL_CUDA(launch_attention_q8(c, q, B, *kv8, seq, len, 1, true, o, ws + L8->att, st),
+              "8-bit decode attention");
+  }
   // P6 (+ the row sums of squares of h for P7)
   DecGemmArgs r{};
   r.B = B; r.eps = a.eps;
@@ -585,6 +647,17 @@ int prepare_decode(const q3vl_config& c, const int32_t* pos, int32_t B, char* ws
 
 }  // namespace
 }  // namespace q3vl
+
+// Runs an entry point's body; an exception (a failed host allocation) becomes
+// a status, so that none crosses the C boundary.
+template <typename F>
+static int no_throw(F&& body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return Q3VL_ECUDA;
+  }
+}
 
 #define ST(s) reinterpret_cast<cudaStream_t>(s)
 
@@ -768,7 +841,8 @@ int q3vl_final_norm(const q3vl_config* cfg, void* x, int64_t S, const void* gain
 static int layer_prefill_impl(const q3vl_config* cfg, const q3vl_layer* layer, void* x, int64_t S,
                               const int32_t* pos, const void* ds_slab, const int32_t* ds_rows,
                               int32_t n_img, const q3vl_kv_cache* kv, int32_t kv_seq, void* ws,
-                              size_t ws_bytes, q3vl_stream stream) {
+                              size_t ws_bytes, q3vl_stream stream,
+                              const q3vl_kv_cache_q8* kv8 = nullptr) {
   Q3VL_TRY(check_cfg(cfg));
   Q3VL_TRY(check_seq(S));
   Q3VL_TRY(check_layer(cfg, layer));
@@ -791,7 +865,7 @@ static int layer_prefill_impl(const q3vl_config* cfg, const q3vl_layer* layer, v
               "deepstack map");
   stage_event(1, st);
   return run_layer(*cfg, *layer, x, S, w, L, ds_slab, st, false, false, kv, kv_seq,
-                   is_bf16(*cfg));
+                   is_bf16(*cfg), kv8);
 }
 
 // Cache checks of the *_kv prefill calls: bf16, rows 0..S-1 of one slot.
@@ -829,7 +903,8 @@ static int stack_prefill_impl(const q3vl_config* cfg, int32_t n_layers, const q3
                               const void* final_norm, void* x, int64_t S, const int32_t* pos,
                               const void* const* ds_slabs, int32_t n_ds, const int32_t* ds_rows,
                               int32_t n_img, const q3vl_kv_cache* kv, int32_t kv_seq, void* ws,
-                              size_t ws_bytes, q3vl_stream stream) {
+                              size_t ws_bytes, q3vl_stream stream,
+                              const q3vl_kv_cache_q8* kv8 = nullptr) {
   Q3VL_TRY(check_cfg(cfg));
   Q3VL_TRY(check_seq(S));
   if (n_layers <= 0 || layers == nullptr)
@@ -866,7 +941,8 @@ static int stack_prefill_impl(const q3vl_config* cfg, int32_t n_layers, const q3
     const void* slab = l < n_ds ? ds_slabs[l] : nullptr;
     // P2 of layer l > 0 comes from layer l-1's down epilogue
     const int rc = run_layer(*cfg, layers[l], x, S, w, L, slab, st, l > 0, l + 1 < n_layers,
-                             kv != nullptr ? kv + l : nullptr, kv_seq, l == 0 && is_bf16(*cfg));
+                             kv != nullptr ? kv + l : nullptr, kv_seq, l == 0 && is_bf16(*cfg),
+                             kv8 != nullptr ? kv8 + l : nullptr);
     if (rc != Q3VL_OK) g_stage_events_on = events;
     if (rc != Q3VL_OK) return set_error(rc, "layer " + std::to_string(l) + ": " + g_last_error);
   }
@@ -931,7 +1007,7 @@ int q3vl_layer_decode(const q3vl_config* cfg, const q3vl_layer* layer, void* x, 
   const DecLayout L = dec_layout(*cfg, B, kv->cap);
   char* w = static_cast<char*>(ws);
   Q3VL_TRY(prepare_decode(*cfg, pos, B, w, L, st));
-  return run_decode_layer(*cfg, *layer, x, B, *kv, seq, len, w, L, st, false, false);
+  return run_decode_layer(*cfg, *layer, x, B, kv, seq, len, w, L, st, false, false);
 }
 
 int q3vl_stack_decode(const q3vl_config* cfg, int32_t n_layers, const q3vl_layer* layers,
@@ -948,7 +1024,7 @@ int q3vl_stack_decode(const q3vl_config* cfg, int32_t n_layers, const q3vl_layer
   char* w = static_cast<char*>(ws);
   Q3VL_TRY(prepare_decode(*cfg, pos, B, w, L, st));
   for (int32_t l = 0; l < n_layers; ++l) {
-    const int rc = run_decode_layer(*cfg, layers[l], x, B, kv[l], seq, len, w, L, st, l > 0,
+    const int rc = run_decode_layer(*cfg, layers[l], x, B, kv + l, seq, len, w, L, st, l > 0,
                                     l + 1 < n_layers);
     if (rc != Q3VL_OK) return set_error(rc, "layer " + std::to_string(l) + ": " + g_last_error);
   }
@@ -1014,6 +1090,287 @@ int q3vl_lm_head(const q3vl_config* cfg, const void* x, int32_t B, const void* f
   a.W = weight; a.rows = vocab; a.K = cfg->hidden; a.X = ws; a.B = B;
   a.N = vocab; a.out = logits;
   return cuda_check(launch_decode_gemm(Epi::kPlain, a, st), "lm head");
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit serving
+// ---------------------------------------------------------------------------
+static int check_gap_free(const void* a, size_t an, const void* b, size_t bn, const char* what) {
+  const char* a0 = static_cast<const char*>(a);
+  const char* b0 = static_cast<const char*>(b);
+  if (a != nullptr && b != nullptr && a0 < b0 + bn && b0 < a0 + an)
+    return set_error(Q3VL_EINVAL, std::string(what) + " must not overlap an input");
+  return Q3VL_OK;
+}
+
+int q3vl_add_rms_norm_q8(const q3vl_config* cfg, const void* x, const void* delta, int64_t S,
+                         const void* gain, void* h, uint8_t* q, uint8_t* scales,
+                         q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    Q3VL_TRY(check_cfg(cfg));
+    Q3VL_TRY(check_seq(S));
+    if (cfg->hidden > 32768)
+      return set_error(Q3VL_EUNSUPPORTED, "the 8-bit norm needs hidden <= 32768");
+    Q3VL_TRY(check_ptr(x, "x"));
+    if (delta != nullptr) {
+      Q3VL_TRY(check_ptr(delta, "delta"));
+      Q3VL_TRY(check_ptr(h, "h"));
+    }
+    if (gain != nullptr) Q3VL_TRY(check_ptr(gain, "gain"));
+    Q3VL_TRY(check_ptr(q, "q"));
+    Q3VL_TRY(check_ptr(scales, "scales", false));
+    return cuda_check(launch_add_rms_norm_q8(*cfg, x, delta, S, gain, h, q, scales, ST(stream)),
+                      "8-bit norm");
+  });
+}
+
+int q3vl_quantize_weight_q8(const q3vl_config* cfg, const void* w, int64_t N, int64_t K,
+                            uint8_t* wq, uint8_t* ws, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    Q3VL_TRY(check_cfg(cfg));
+    if (N < 1 || N > (int64_t(1) << 30)) return set_error(Q3VL_EINVAL, "N must be in [1, 2^30]");
+    if (K < 64 || K % 64 != 0 || K > (int64_t(1) << 22))
+      return set_error(Q3VL_EINVAL, "K must be a multiple of 64 up to 2^22");
+    Q3VL_TRY(check_ptr(w, "w"));
+    Q3VL_TRY(check_ptr(wq, "wq"));
+    Q3VL_TRY(check_ptr(ws, "ws", false));
+    return cuda_check(launch_quantize_weight_q8(*cfg, w, N, K, wq, ws, ST(stream)),
+                      "8-bit weight");
+  });
+}
+
+static int linear_q8_impl(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
+                          const uint8_t* ws, int64_t N, int64_t K, const void* resid, void* out,
+                          int32_t out_dtype, q3vl_stream stream) {
+  if (M < 1 || M > (int64_t(1) << 30)) return set_error(Q3VL_EINVAL, "M must be in [1, 2^30]");
+  if (N < 1 || N > (int64_t(1) << 30)) return set_error(Q3VL_EINVAL, "N must be in [1, 2^30]");
+  if (K < 64 || K % 64 != 0 || K > (int64_t(1) << 22))
+    return set_error(Q3VL_EINVAL, "K must be a multiple of 64 up to 2^22");
+  if (out_dtype != Q3VL_DTYPE_FP32 && out_dtype != Q3VL_DTYPE_BF16)
+    return set_error(Q3VL_EUNSUPPORTED, "out_dtype must be Q3VL_DTYPE_FP32 or Q3VL_DTYPE_BF16");
+  Q3VL_TRY(check_ptr(xq, "xq"));
+  Q3VL_TRY(check_ptr(xs, "xs", false));
+  Q3VL_TRY(check_ptr(wq, "wq"));
+  Q3VL_TRY(check_ptr(ws, "ws", false));
+  Q3VL_TRY(check_ptr(out, "out"));
+  if (resid != nullptr) Q3VL_TRY(check_ptr(resid, "resid"));
+  const size_t ob = size_t(M) * N * (out_dtype == Q3VL_DTYPE_BF16 ? 2 : 4);
+  Q3VL_TRY(check_gap_free(out, ob, xq, size_t(M) * K, "out"));
+  Q3VL_TRY(check_gap_free(out, ob, wq, size_t(N) * K, "out"));
+  if (resid != out) Q3VL_TRY(check_gap_free(out, ob, resid, ob, "out (unless it is resid)"));
+  return cuda_check(launch_linear_q8(xq, xs, M, wq, ws, N, K, resid, out,
+                                     out_dtype == Q3VL_DTYPE_BF16, ST(stream)),
+                    "8-bit product");
+}
+
+int q3vl_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
+                   const uint8_t* ws, int64_t N, int64_t K, const void* resid, void* out,
+                   int32_t out_dtype, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    return linear_q8_impl(xq, xs, M, wq, ws, N, K, resid, out, out_dtype, stream);
+  });
+}
+
+size_t q3vl_lm_head_q8_workspace_bytes(const q3vl_config* cfg, int32_t B) {
+  if (check_cfg(cfg) != Q3VL_OK || cfg->dtype != Q3VL_DTYPE_BF16 ||
+      check_batch(B) != Q3VL_OK || cfg->hidden > 32768)
+    return 0;
+  const size_t kb = (cfg->hidden + kQ8Block - 1) / kQ8Block;
+  return align256(size_t(B) * cfg->hidden) + align256(size_t(B) * kb);
+}
+
+int q3vl_lm_head_q8(const q3vl_config* cfg, const void* x, int32_t B, const void* final_norm,
+                    const uint8_t* wq, const uint8_t* ws, int64_t vocab, float* logits,
+                    void* wsp, size_t wsp_bytes, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    Q3VL_TRY(check_cfg(cfg));
+    if (cfg->dtype != Q3VL_DTYPE_BF16)
+      return set_error(Q3VL_EUNSUPPORTED, "the LM head is bf16 only");
+    if (cfg->hidden > 32768)
+      return set_error(Q3VL_EUNSUPPORTED, "the 8-bit norm needs hidden <= 32768");
+    Q3VL_TRY(check_batch(B));
+    Q3VL_TRY(check_ptr(x, "x"));
+    if (final_norm != nullptr) Q3VL_TRY(check_ptr(final_norm, "final_norm"));
+    const size_t need = q3vl_lm_head_q8_workspace_bytes(cfg, B);
+    if (wsp == nullptr || (reinterpret_cast<uintptr_t>(wsp) & 255) != 0 || wsp_bytes < need)
+      return set_error(Q3VL_EWORKSPACE, "8-bit lm head workspace too small: need " +
+                                            std::to_string(need) + " bytes, 256-byte aligned");
+    uint8_t* q = static_cast<uint8_t*>(wsp);
+    uint8_t* s = q + align256(size_t(B) * cfg->hidden);
+    Q3VL_CUDA(launch_add_rms_norm_q8(*cfg, x, nullptr, B, final_norm, nullptr, q, s, ST(stream)),
+              "8-bit lm head norm");
+    return linear_q8_impl(q, s, B, wq, ws, vocab, cfg->hidden, nullptr, logits, Q3VL_DTYPE_FP32,
+                          stream);
+  });
+}
+
+static int check_q8_cfg(const q3vl_config* cfg) {
+  Q3VL_TRY(check_cfg(cfg));
+  if (cfg->dtype != Q3VL_DTYPE_BF16)
+    return set_error(Q3VL_EUNSUPPORTED, "the 8-bit cache calls are for bf16 configs");
+  return Q3VL_OK;
+}
+
+static int check_group(const q3vl_config* cfg) {
+  const int G = cfg->n_heads / cfg->n_kv_heads;
+  if (G != 1 && G != 2 && G != 4 && G != 8)
+    return set_error(Q3VL_EUNSUPPORTED, "decode needs n_heads / n_kv_heads in {1, 2, 4, 8}");
+  return Q3VL_OK;
+}
+
+int q3vl_kv_store_q8(const q3vl_config* cfg, const void* k, const void* v, int64_t ld, int64_t T,
+                     const int32_t* starts, int32_t B, const q3vl_kv_cache_q8* kv,
+                     const int32_t* seq, const int32_t* len, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    Q3VL_TRY(check_q8_cfg(cfg));
+    Q3VL_TRY(check_batch(B));
+    Q3VL_TRY(check_ptr(k, "k"));
+    Q3VL_TRY(check_ptr(v, "v"));
+    if (ld < kv_dim(*cfg) || ld % 8 != 0)
+      return set_error(Q3VL_EINVAL, "ld must be a multiple of 8 and at least nkv*hd");
+    if (T < 1 || T > (int64_t(1) << 30)) return set_error(Q3VL_EINVAL, "T must be in [1, 2^30]");
+    if (starts == nullptr && T != B)
+      return set_error(Q3VL_EINVAL, "without starts, T must be B (one row per sequence)");
+    Q3VL_TRY(check_kv_q8(kv, "kv"));
+    Q3VL_TRY(check_ptr(seq, "seq", false));
+    Q3VL_TRY(check_ptr(len, "len", false));
+    return cuda_check(launch_kv_store_q8(*cfg, k, v, ld, T, starts, B, *kv, seq, len, 0,
+                                         ST(stream)),
+                      "8-bit kv cache store");
+  });
+}
+
+size_t q3vl_attention_q8_workspace_bytes(const q3vl_config* cfg, int32_t B, int64_t cap) {
+  if (check_q8_cfg(cfg) != Q3VL_OK || check_group(cfg) != Q3VL_OK || check_batch(B) != Q3VL_OK ||
+      check_kv_size(cap, 1) != Q3VL_OK)
+    return 0;
+  return attention_q8_ws_bytes(*cfg, B, cap);
+}
+
+int q3vl_attention_q8(const q3vl_config* cfg, const void* q, int32_t B,
+                      const q3vl_kv_cache_q8* kv, const int32_t* seq, const int32_t* len, void* o,
+                      void* ws, size_t ws_bytes, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    Q3VL_TRY(check_q8_cfg(cfg));
+    Q3VL_TRY(check_group(cfg));
+    Q3VL_TRY(check_batch(B));
+    Q3VL_TRY(check_ptr(q, "q"));
+    Q3VL_TRY(check_kv_q8(kv, "kv"));
+    Q3VL_TRY(check_ptr(seq, "seq", false));
+    Q3VL_TRY(check_ptr(len, "len", false));
+    Q3VL_TRY(check_ptr(o, "o"));
+    const size_t need = attention_q8_ws_bytes(*cfg, B, kv->cap);
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) != 0 || ws_bytes < need)
+      return set_error(Q3VL_EWORKSPACE, "8-bit attention workspace too small: need " +
+                                            std::to_string(need) + " bytes, 256-byte aligned");
+    return cuda_check(launch_attention_q8(*cfg, q, B, *kv, seq, len, 0, false, o, ws, ST(stream)),
+                      "8-bit attention");
+  });
+}
+
+static int check_prefill_kv_q8(const q3vl_config* cfg, int64_t S, const q3vl_kv_cache_q8* kv,
+                               int32_t n, int32_t seq) {
+  Q3VL_TRY(check_q8_cfg(cfg));
+  if (kv == nullptr) return set_error(Q3VL_EINVAL, "kv is NULL");
+  for (int32_t l = 0; l < n; ++l) {
+    Q3VL_TRY(check_kv_q8(kv + l, "kv"));
+    if (S > kv[l].cap) return set_error(Q3VL_ERANGE, "S exceeds the cache capacity");
+    if (seq < 0 || seq >= kv[l].n_seq) return set_error(Q3VL_ERANGE, "seq outside [0, n_seq)");
+  }
+  return Q3VL_OK;
+}
+
+int q3vl_layer_prefill_kv_q8(const q3vl_config* cfg, const q3vl_layer* layer, void* x, int64_t S,
+                             const int32_t* pos, const void* ds_slab, const int32_t* ds_rows,
+                             int32_t n_img, const q3vl_kv_cache_q8* kv, int32_t seq, void* ws,
+                             size_t ws_bytes, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    Q3VL_TRY(check_prefill_kv_q8(cfg, S, kv, 1, seq));
+    return layer_prefill_impl(cfg, layer, x, S, pos, ds_slab, ds_rows, n_img, nullptr, seq, ws,
+                              ws_bytes, stream, kv);
+  });
+}
+
+int q3vl_stack_prefill_kv_q8(const q3vl_config* cfg, int32_t n_layers, const q3vl_layer* layers,
+                             const void* final_norm, void* x, int64_t S, const int32_t* pos,
+                             const void* const* ds_slabs, int32_t n_ds, const int32_t* ds_rows,
+                             int32_t n_img, const q3vl_kv_cache_q8* kv, int32_t seq, void* ws,
+                             size_t ws_bytes, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    if (n_layers <= 0) return set_error(Q3VL_EINVAL, "n_layers must be >= 1");
+    Q3VL_TRY(check_prefill_kv_q8(cfg, S, kv, n_layers, seq));
+    return stack_prefill_impl(cfg, n_layers, layers, final_norm, x, S, pos, ds_slabs, n_ds,
+                              ds_rows, n_img, nullptr, seq, ws, ws_bytes, stream, kv);
+  });
+}
+
+size_t q3vl_decode_q8_workspace_bytes(const q3vl_config* cfg, int32_t B, int64_t cap) {
+  if (check_cfg(cfg) != Q3VL_OK || check_decode_cfg(*cfg) != Q3VL_OK || check_batch(B) != Q3VL_OK ||
+      check_kv_size(cap, 1) != Q3VL_OK)
+    return 0;
+  return dec_q8_layout(*cfg, B, cap).total;
+}
+
+static int decode_q8_impl(const q3vl_config* cfg, int32_t n_layers, const q3vl_layer* layers,
+                          const void* final_norm, void* x, int32_t B, const int32_t* pos,
+                          const q3vl_kv_cache_q8* kv, const int32_t* seq, const int32_t* len,
+                          void* ws, size_t ws_bytes, q3vl_stream stream) {
+  Q3VL_TRY(check_cfg(cfg));
+  Q3VL_TRY(check_decode_cfg(*cfg));
+  Q3VL_TRY(check_batch(B));
+  if (layers == nullptr || kv == nullptr) return set_error(Q3VL_EINVAL, "layers / kv are NULL");
+  int64_t cap = 0;
+  for (int32_t l = 0; l < n_layers; ++l) {
+    const int rc = check_layer(cfg, layers + l);
+    if (rc != Q3VL_OK) return set_error(rc, "layer " + std::to_string(l) + ": " + g_last_error);
+    Q3VL_TRY(check_kv_q8(kv + l, "kv"));
+    if (kv[l].cap > cap) cap = kv[l].cap;
+  }
+  Q3VL_TRY(check_ptr(x, "x"));
+  Q3VL_TRY(check_ptr(pos, "pos", false));
+  Q3VL_TRY(check_ptr(seq, "seq", false));
+  Q3VL_TRY(check_ptr(len, "len", false));
+  if (final_norm != nullptr) Q3VL_TRY(check_ptr(final_norm, "final_norm"));
+  const DecQ8Layout L = dec_q8_layout(*cfg, B, cap);
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) != 0)
+    return set_error(Q3VL_EWORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (ws_bytes < L.total)
+    return set_error(Q3VL_EWORKSPACE, "8-bit decode workspace too small: need " +
+                                          std::to_string(L.total) + " bytes, got " +
+                                          std::to_string(ws_bytes));
+  const cudaStream_t st = ST(stream);
+  char* w = static_cast<char*>(ws);
+  Q3VL_TRY(prepare_decode(*cfg, pos, B, w, L.d, st));
+  Q3VL_CUDA(launch_iota_zero(B, reinterpret_cast<int32_t*>(w + L.iota),
+                             reinterpret_cast<int32_t*>(w + L.zero), st),
+            "8-bit decode indexes");
+  for (int32_t l = 0; l < n_layers; ++l) {
+    const int rc = run_decode_layer(*cfg, layers[l], x, B, nullptr, seq, len, w, L.d, st, l > 0,
+                                    l + 1 < n_layers, kv + l, &L);
+    if (rc != Q3VL_OK) return set_error(rc, "layer " + std::to_string(l) + ": " + g_last_error);
+  }
+  if (final_norm != nullptr)
+    Q3VL_CUDA(launch_final_norm(*cfg, x, B, final_norm, st), "final norm");
+  return Q3VL_OK;
+}
+
+int q3vl_layer_decode_q8(const q3vl_config* cfg, const q3vl_layer* layer, void* x, int32_t B,
+                         const int32_t* pos, const q3vl_kv_cache_q8* kv, const int32_t* seq,
+                         const int32_t* len, void* ws, size_t ws_bytes, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    return decode_q8_impl(cfg, 1, layer, nullptr, x, B, pos, kv, seq, len, ws, ws_bytes, stream);
+  });
+}
+
+int q3vl_stack_decode_q8(const q3vl_config* cfg, int32_t n_layers, const q3vl_layer* layers,
+                         const void* final_norm, void* x, int32_t B, const int32_t* pos,
+                         const q3vl_kv_cache_q8* kv, const int32_t* seq, const int32_t* len,
+                         void* ws, size_t ws_bytes, q3vl_stream stream) {
+  return no_throw([&]() -> int {
+    if (n_layers <= 0) return set_error(Q3VL_EINVAL, "n_layers must be >= 1");
+    return decode_q8_impl(cfg, n_layers, layers, final_norm, x, B, pos, kv, seq, len, ws, ws_bytes,
+                          stream);
+  });
 }
 
 int q3vl_decode_advance(int32_t B, int32_t* pos, int32_t* len, q3vl_stream stream) {

@@ -22,10 +22,11 @@ enum WhereTag : int32_t {
   kWherePositions = 301, kWhereDeepstackMap = 302, kWhereEmbed = 303, kWhereSelftest = 401,
   kWhereDecodeProducer = 501, kWhereDecodeMma = 502, kWhereDecodeEpilogue = 503,
   kWhereDecodeRange = 504, kWhereDecodeAttn = 505,
+  kWhereStoreQ8Range = 701, kWhereAttnQ8Range = 702, kWhereAttnQ8 = 703, kWhereLinearQ8 = 704,
   // bounds checks of the debug build (-DQ3VL_DEBUG)
   kWhereDbgAttnStore = 601, kWhereDbgGemmScratch = 602, kWhereDbgGemmRowsq = 603,
   kWhereDbgPositions = 604, kWhereDbgTable = 605, kWhereDbgRowstat = 606,
-  kWhereDbgDecodeStore = 607,
+  kWhereDbgDecodeStore = 607, kWhereDbgQ8 = 608,
 };
 
 // Error record: [0] = status code, [1] = location tag. First error wins.

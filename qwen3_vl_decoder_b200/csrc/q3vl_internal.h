@@ -199,6 +199,33 @@ cudaError_t launch_kv_store(const q3vl_config& c, const void* qkv, int64_t S,
                             const q3vl_kv_cache& kv, int32_t seq, cudaStream_t st);
 cudaError_t launch_decode_advance(int B, int32_t* pos, int32_t* len, cudaStream_t st);
 
+// 8-bit serving (q8_rows.cu, linear_q8.cu, attn_q8.cu).
+constexpr int kQ8Block = 128;   // columns, weight rows or tokens that share a scale
+cudaError_t launch_add_rms_norm_q8(const q3vl_config& c, const void* x, const void* delta, int64_t S,
+                                   const void* gain, void* h, uint8_t* q, uint8_t* scales,
+                                   cudaStream_t st);
+cudaError_t launch_quantize_weight_q8(const q3vl_config& c, const void* w, int64_t N, int64_t K,
+                                      uint8_t* wq, uint8_t* ws, cudaStream_t st);
+cudaError_t launch_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
+                             const uint8_t* ws, int64_t N, int64_t K, const void* resid, void* out,
+                             bool out_bf16, cudaStream_t st);
+// Rows of B sequences into the 8-bit cache. seq == nullptr: B = 1, all T rows
+// to rows 0.. of slot seq0. starts == nullptr with seq: one row per sequence.
+cudaError_t launch_kv_store_q8(const q3vl_config& c, const void* k, const void* v, int64_t ld,
+                               int64_t T, const int32_t* starts, int B,
+                               const q3vl_kv_cache_q8& kv, const int32_t* seq, const int32_t* len,
+                               int32_t seq0, cudaStream_t st);
+size_t attention_q8_ws_bytes(const q3vl_config& c, int B, int64_t cap);
+// `plus`: 1 = rows 0..len[b] (the new row was just appended), 0 = rows
+// 0..len[b]-1. `early`: the full blocks below len[b] were written before this
+// call's first kernel, so they may be read before the kernel's own dependency.
+cudaError_t launch_attention_q8(const q3vl_config& c, const void* q, int B,
+                                const q3vl_kv_cache_q8& kv, const int32_t* seq,
+                                const int32_t* len, int plus, bool early, void* o, void* ws,
+                                cudaStream_t st);
+// Indexes of a one-row-per-sequence scratch "cache": iota[b] = b, zero[b] = 0.
+cudaError_t launch_iota_zero(int B, int32_t* iota, int32_t* zero, cudaStream_t st);
+
 // Launches `kernel` on `st` as a programmatic dependent of the kernel before
 // it in the stream (PDL): it may start while that kernel finishes, and must
 // call griddepcontrol.wait before it touches memory that kernel, or any

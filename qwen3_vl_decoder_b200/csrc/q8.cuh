@@ -1,0 +1,95 @@
+// 8-bit blocks: e4m3 elements with a power-of-two scale per block, held as an
+// E8M0 byte u (the scale is 2^(u - 127)).
+//
+// A power of two costs no precision against a free scale as long as a block's
+// values stay above e4m3's subnormals (2^-15 of the block's maximum): dividing
+// by it is exact, so each element is rounded once, by at most 2^-4 of its
+// value. It lets the tensor core apply the scales itself, and a cache block
+// can move to a larger scale without touching the mantissas of its elements.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "q3vl_device.cuh"
+
+namespace q3vl {
+
+// E8M0 byte of the scale for a block maximum `amax` (finite, >= 0): the
+// smallest s >= -126 with amax <= 448 2^s = 1.75 2^(s + 8). With amax =
+// m 2^e, 1 <= m < 2, that is s = e - 8, or e - 7 when m > 1.75.
+__device__ __forceinline__ uint32_t e8m0_of_amax(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int u = static_cast<int>(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return static_cast<uint32_t>(u < 1 ? 1 : u);
+}
+
+// 2^(u - 127) and 2^(127 - u) for u in [1, 253] (a scale made by
+// e8m0_of_amax is at most 2^120).
+__device__ __forceinline__ float e8m0_scale(uint32_t u) { return __uint_as_float(u << 23); }
+__device__ __forceinline__ float e8m0_inverse(uint32_t u) {
+  return __uint_as_float((254u - u) << 23);
+}
+
+// |x| where x is finite, else 0: what x adds to its block's maximum.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.f;
+}
+
+// Four floats (already divided by the scale) to e4m3, round to nearest even,
+// element 0 in the low byte. fma(x, 0, x) turns an infinity into NaN (the
+// conversion alone would saturate it) and leaves finite values as they are.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  a = fmaf(a, 0.f, a); b = fmaf(b, 0.f, b); c = fmaf(c, 0.f, c); d = fmaf(d, 0.f, d);
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// Four e4m3 bytes to floats.
+__device__ __forceinline__ float4 unpack_e4m3x4(uint32_t w) {
+  uint32_t l, h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(l) : "h"(static_cast<uint16_t>(w & 0xffffu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w >> 16)));
+  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&l));
+  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&h));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Eight consecutive elements of a row as floats (16-byte aligned address).
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 t = unpack_bf16x2(w[j]);
+    f[2 * j] = t.x;
+    f[2 * j + 1] = t.y;
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// Rounds to the row's type and stores; f becomes the rounded values.
+__device__ __forceinline__ void store8(__nv_bfloat16* p, float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+    const float2 t = unpack_bf16x2(w[j]);
+    f[2 * j] = t.x;
+    f[2 * j + 1] = t.y;
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, float (&f)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+}  // namespace q3vl

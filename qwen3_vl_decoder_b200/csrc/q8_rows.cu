@@ -1,0 +1,323 @@
+// Making 8-bit blocks (q8.cuh): activation rows behind a residual add and
+// RMSNorm, weight matrices, and K/V rows into the 8-bit cache.
+#include "q3vl_internal.h"
+#include "q8.cuh"
+
+namespace q3vl {
+namespace {
+
+// ---------------------------------------------------------------------------
+// h = x + delta; y = h * (1 / rms(h)) * gain; e4m3 of y, a scale per 128
+// columns. One block per row; a thread takes units of 8 columns, so 16
+// neighbouring threads hold one block of 128 and its maximum is four shuffles.
+// The row stays in registers between the sum of squares (fp32) and the
+// rounding: every input is read once. Bound by memory: 7 bytes per bf16
+// element with a delta (3 without).
+// ---------------------------------------------------------------------------
+template <typename T, int NV>
+__global__ void __launch_bounds__(1024)
+add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t* q,
+                       uint8_t* scales, int width, int nblk, float eps) {
+  const int t = threadIdx.x, lane = t & 31;
+  const int64_t row = blockIdx.x;
+  const int units = width / 8;
+  const T* xr = x + row * width;
+  griddep_launch_dependents();
+  griddep_wait();
+  float f[NV][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int u = t + i * blockDim.x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
+    if (u < units) {
+      load8(xr + 8 * u, f[i]);
+      if (delta != nullptr) {
+        float d[8];
+        load8(delta + row * width + 8 * u, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] += d[j];
+        store8(h + row * width + 8 * u, f[i]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
+  }
+  float inv = 1.f;
+  if (gain != nullptr) {
+    __shared__ float s_ss[32];
+    ss = warp_sum(ss);
+    if (lane == 0) s_ss[t >> 5] = ss;
+    __syncthreads();
+    ss = lane < (blockDim.x >> 5) ? s_ss[lane] : 0.f;
+    ss = warp_sum(ss);
+    inv = 1.0f / sqrtf(ss / static_cast<float>(width) + eps);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int u = t + i * blockDim.x;
+    if (gain != nullptr && u < units) {
+      float g[8];
+      load8(gain + 8 * u, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * inv * g[j];
+    }
+    float a = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(f[i][j]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    const uint32_t e = e8m0_of_amax(a);
+    const float s = e8m0_inverse(e);
+    if (u < units) {
+      uint2 w;
+      w.x = pack_e4m3x4(f[i][0] * s, f[i][1] * s, f[i][2] * s, f[i][3] * s);
+      w.y = pack_e4m3x4(f[i][4] * s, f[i][5] * s, f[i][6] * s, f[i][7] * s);
+      *reinterpret_cast<uint2*>(q + row * width + 8 * u) = w;
+      if ((t & 15) == 0) scales[row * nblk + u / 16] = static_cast<uint8_t>(e);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Weights: one block of 256 threads per 128 x 128 block, whose elements stay
+// in registers between the maximum and the rounding.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256)
+quantize_weight_kernel(const T* __restrict__ w, int64_t N, int64_t K, uint8_t* __restrict__ wq,
+                       uint8_t* __restrict__ ws) {
+  const int t = threadIdx.x, lane = t & 31;
+  const int64_t kblk = (K + 127) / 128;
+  const int64_t nb = blockIdx.x / kblk, kb = blockIdx.x % kblk;
+  const int64_t col = kb * 128 + (t & 15) * 8;
+  float f[8][8];
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = nb * 128 + (t >> 4) + 16 * i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
+    if (row < N && col < K) load8(w + row * K + col, f[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(f[i][j]));
+  }
+  __shared__ float s_a[8];
+  a = warp_max(a);
+  if (lane == 0) s_a[t >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, s_a[i]);
+  const uint32_t e = e8m0_of_amax(a);
+  const float s = e8m0_inverse(e);
+  if (t == 0) ws[nb * kblk + kb] = static_cast<uint8_t>(e);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = nb * 128 + (t >> 4) + 16 * i;
+    if (row < N && col < K) {
+      uint2 v;
+      v.x = pack_e4m3x4(f[i][0] * s, f[i][1] * s, f[i][2] * s, f[i][3] * s);
+      v.y = pack_e4m3x4(f[i][4] * s, f[i][5] * s, f[i][6] * s, f[i][7] * s);
+      *reinterpret_cast<uint2*>(wq + row * K + col) = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows into the 8-bit cache. A work item is one (sequence, 128-token block,
+// KV head, K or V); its new rows stay in registers between the maximum and
+// the rounding. The items of sequence b sit at floor(starts[b] / 128) + 2 b
+// along grid x: n rows touch at most floor(n / 128) + 2 blocks, so the items
+// of two sequences never meet and no scan is needed; a place that no item
+// takes exits. Bound by memory: 3 bytes per element.
+// ---------------------------------------------------------------------------
+struct StoreQ8Params {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t ld, T;
+  const int32_t* starts;  // [B + 1] or null: one row per sequence (seq given), or all T rows
+  int B;
+  const int32_t* seq;     // [B] or null: slot seq0, from row 0
+  const int32_t* len;     // [B]
+  int32_t seq0;
+  uint8_t* kc;
+  uint8_t* vc;
+  uint8_t* ks;
+  uint8_t* vs;
+  int64_t cap;
+  int n_seq, nkv;
+  int32_t* err;
+};
+
+__global__ void __launch_bounds__(256) kv_store_q8_kernel(StoreQ8Params p) {
+  const int t = threadIdx.x, lane = t & 31;
+  __shared__ int s_item[4];  // slot (-1: none), rows cached, first source row, rows
+  __shared__ int s_blk;
+  __shared__ float s_a[8];
+  if (t == 0) s_item[0] = -1;
+  griddep_launch_dependents();
+  griddep_wait();
+  __syncthreads();
+  // Starts that decrease would let two sequences claim one place: then nothing
+  // is stored. B <= 256: one sequence per thread.
+  bool falls = false;
+  if (t < p.B) {
+    const int b = t;
+    int slot, len, s0, n;
+    if (p.seq == nullptr) {
+      slot = p.seq0; len = 0; s0 = 0; n = static_cast<int>(p.T);
+    } else {
+      slot = p.seq[b];
+      len = p.len[b];
+      s0 = p.starts ? p.starts[b] : b;
+      n = (p.starts ? p.starts[b + 1] : b + 1) - s0;
+    }
+    falls = n < 0;
+    const bool ok = slot >= 0 && slot < p.n_seq && len >= 0 && n >= 0 && s0 >= 0 &&
+                    int64_t(s0) + n <= p.T && int64_t(len) + n <= p.cap;
+    if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+      record_error(p.err, Q3VL_ERANGE, kWhereStoreQ8Range);
+    const int64_t base = p.starts ? int64_t(s0) / 128 + 2 * b : b;
+    const int64_t j = int64_t(blockIdx.x) - base;
+    if (ok && n > 0 && j >= 0 && j <= (len + n - 1) / 128 - len / 128) {
+      s_item[0] = slot; s_item[1] = len; s_item[2] = s0; s_item[3] = n;
+      s_blk = len / 128 + static_cast<int>(j);
+    }
+  }
+  if (__syncthreads_or(falls ? 1 : 0)) return;
+  const int slot = s_item[0];
+  if (slot < 0) return;
+  const int len = s_item[1], n = s_item[3], blk = s_blk;
+  const int g = blockIdx.y;
+  const __nv_bfloat16* src = (blockIdx.z == 0 ? p.k : p.v) + int64_t(g) * 128 + (t & 15) * 8;
+  uint8_t* cache = blockIdx.z == 0 ? p.kc : p.vc;
+  const int64_t nblk = (p.cap + 127) / 128;
+  uint8_t* scale = (blockIdx.z == 0 ? p.ks : p.vs) + (int64_t(slot) * nblk + blk) * p.nkv + g;
+  const int lo = max(len, blk * 128), hi = min(len + n, blk * 128 + 128);
+  const int64_t s0 = int64_t(s_item[2]) + (lo - len);
+  float f[8][8];
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = (t >> 4) + 16 * i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
+    if (lo + r < hi && dcheck(s0 + r < p.T, p.err, kWhereDbgQ8)) load8(src + (s0 + r) * p.ld, f[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(f[i][j]));
+  }
+  a = warp_max(a);
+  if (lane == 0) s_a[t >> 5] = a;
+  const bool keeps = blk * 128 < len;  // the block holds earlier rows
+  const uint32_t was = keeps ? *scale : 0u;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, s_a[i]);
+  uint32_t e = e8m0_of_amax(a);
+  if (keeps && was >= e) e = was;
+  if (t == 0) *scale = static_cast<uint8_t>(e);
+  const int64_t rs = int64_t(p.nkv) * 128;
+  uint8_t* dst = cache + (int64_t(slot) * p.cap) * rs + int64_t(g) * 128 + (t & 15) * 8;
+  if (keeps && e > was) {
+    // the earlier rows move to the larger scale: a shift of the exponent, and
+    // a rounding of what falls among e4m3's subnormals
+    const float m = e - was > 126 ? 0.f : e8m0_inverse(127 + (e - was));
+    for (int r = blk * 128 + (t >> 4); r < len; r += 16) {
+      uint2 w = *reinterpret_cast<uint2*>(dst + r * rs);
+      const float4 x = unpack_e4m3x4(w.x), y = unpack_e4m3x4(w.y);
+      w.x = pack_e4m3x4(x.x * m, x.y * m, x.z * m, x.w * m);
+      w.y = pack_e4m3x4(y.x * m, y.y * m, y.z * m, y.w * m);
+      *reinterpret_cast<uint2*>(dst + r * rs) = w;
+    }
+  }
+  const float s = e8m0_inverse(e);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = lo + (t >> 4) + 16 * i;
+    if (r < hi && dcheck(r < p.cap, p.err, kWhereDbgQ8)) {
+      uint2 w;
+      w.x = pack_e4m3x4(f[i][0] * s, f[i][1] * s, f[i][2] * s, f[i][3] * s);
+      w.y = pack_e4m3x4(f[i][4] * s, f[i][5] * s, f[i][6] * s, f[i][7] * s);
+      *reinterpret_cast<uint2*>(dst + int64_t(r) * rs) = w;
+    }
+  }
+}
+
+__global__ void iota_zero_kernel(int B, int32_t* iota, int32_t* zero) {
+  const int b = threadIdx.x;
+  if (b >= B) return;
+  iota[b] = b;
+  zero[b] = 0;
+}
+
+template <typename T>
+cudaError_t launch_norm_t(const void* x, const void* delta, int64_t S, const void* gain, void* h,
+                          uint8_t* q, uint8_t* scales, int width, float eps, cudaStream_t st) {
+  const int units = width / 8;
+  const int nblk = (width + kQ8Block - 1) / kQ8Block;
+  auto go = [&](auto kern, int nv) {
+    const int th = ((units + nv - 1) / nv + 31) / 32 * 32;
+    return launch_pdl_plain(kern, dim3(static_cast<unsigned>(S)), dim3(th), 0, st,
+                            static_cast<const T*>(x), static_cast<const T*>(delta),
+                            static_cast<const T*>(gain), static_cast<T*>(h), q, scales, width,
+                            nblk, eps);
+  };
+  cudaError_t e;
+  if (units <= 1024) e = go(add_rms_norm_q8_kernel<T, 1>, 1);
+  else if (units <= 4096) e = go(add_rms_norm_q8_kernel<T, 4>, 4);
+  else return cudaErrorInvalidValue;
+  if (e != cudaSuccess) return e;
+  return counted_launch(1);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rms_norm_q8(const q3vl_config& c, const void* x, const void* delta, int64_t S,
+                                   const void* gain, void* h, uint8_t* q, uint8_t* scales,
+                                   cudaStream_t st) {
+  const float eps = static_cast<float>(c.rms_eps);
+  if (c.dtype == Q3VL_DTYPE_BF16)
+    return launch_norm_t<__nv_bfloat16>(x, delta, S, gain, h, q, scales, c.hidden, eps, st);
+  return launch_norm_t<float>(x, delta, S, gain, h, q, scales, c.hidden, eps, st);
+}
+
+cudaError_t launch_quantize_weight_q8(const q3vl_config& c, const void* w, int64_t N, int64_t K,
+                                      uint8_t* wq, uint8_t* ws, cudaStream_t st) {
+  const int64_t blocks = ((N + 127) / 128) * ((K + 127) / 128);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  if (c.dtype == Q3VL_DTYPE_BF16)
+    quantize_weight_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
+        static_cast<const __nv_bfloat16*>(w), N, K, wq, ws);
+  else
+    quantize_weight_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
+        static_cast<const float*>(w), N, K, wq, ws);
+  return counted_launch(1);
+}
+
+cudaError_t launch_kv_store_q8(const q3vl_config& c, const void* k, const void* v, int64_t ld,
+                               int64_t T, const int32_t* starts, int B,
+                               const q3vl_kv_cache_q8& kv, const int32_t* seq, const int32_t* len,
+                               int32_t seq0, cudaStream_t st) {
+  StoreQ8Params p{};
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.ld = ld; p.T = T; p.starts = starts; p.B = B; p.seq = seq; p.len = len; p.seq0 = seq0;
+  p.kc = kv.k; p.vc = kv.v; p.ks = kv.k_scale; p.vs = kv.v_scale;
+  p.cap = kv.cap; p.n_seq = kv.n_seq; p.nkv = c.n_kv_heads;
+  p.err = device_error_ptr();
+  // places along x: see the kernel's comment
+  const int64_t nx = starts ? T / 128 + 2 * int64_t(B) : (seq ? B : (T + 127) / 128);
+  const cudaError_t e = launch_pdl_plain(
+      kv_store_q8_kernel,
+      dim3(static_cast<unsigned>(nx), static_cast<unsigned>(c.n_kv_heads), 2), dim3(256), 0, st, p);
+  if (e != cudaSuccess) return e;
+  return counted_launch(1);
+}
+
+cudaError_t launch_iota_zero(int B, int32_t* iota, int32_t* zero, cudaStream_t st) {
+  iota_zero_kernel<<<1, 256, 0, st>>>(B, iota, zero);
+  return counted_launch(1);
+}
+
+}  // namespace q3vl
