@@ -61,6 +61,9 @@ int cuda_check(cudaError_t e, const char* what);
 // `ld` elements, box (box_cols x box_rows), 128-byte swizzle, zero fill.
 bool make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols,
                     uint64_t ld, uint32_t box_cols, uint32_t box_rows);
+// The same over a row-major [rows, cols] matrix of bytes.
+bool make_tmap_u8(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
+                  uint32_t box_cols, uint32_t box_rows);
 
 // ---------------------------------------------------------------------------
 // Launchers (all enqueue on `st`, return the launch status).
@@ -230,7 +233,7 @@ cudaError_t launch_iota_zero(int B, int32_t* iota, int32_t* zero, cudaStream_t s
 // it in the stream (PDL): it may start while that kernel finishes, and must
 // call griddepcontrol.wait before it touches memory that kernel, or any
 // earlier one, reads or writes. Compile-time cluster dimensions of the kernel
-// apply as usual.
+// apply as usual; launch_pdl_cluster sets them at run time.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t st, Args&&... args) {
@@ -244,6 +247,26 @@ cudaError_t launch_pdl_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                               cudaStream_t st, int cluster, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 

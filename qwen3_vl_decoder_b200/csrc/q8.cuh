@@ -92,4 +92,67 @@ __device__ __forceinline__ void store8(float* p, float (&f)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
+// ---------------------------------------------------------------------------
+// tcgen05 with block scales (kind::mxf8f6f4: e4m3 operands, one E8M0 scale per
+// row and 32 columns, fp32 accumulation)
+// ---------------------------------------------------------------------------
+// Instruction descriptor: bits [4,6) and [29,31) choose the byte of B's and
+// A's scale words (0 here), [7,10) / [10,13) A / B format (0 = e4m3),
+// [17,23) N >> 3, 23 scale type (1 = E8M0), [24,29) M >> 4.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
+  return (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// D[tmem] (+)= (A 2^sa) (B 2^sb)^T, operands in shared memory, scale words in
+// TMEM (one thread).
+__device__ __forceinline__ void umma_mxf8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+      "[%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+__device__ __forceinline__ void umma_mxf8_ss_pair(uint32_t d_tmem, uint64_t a_desc,
+                                                  uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                                  uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X "
+      "[%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
+// Scale words of 128 operand rows: 512 bytes in shared memory, the word of row
+// r at (r % 32) * 16 + (r / 32) * 4, copied to 4 TMEM columns (row r in lane
+// r % 32 of column r / 32, in all four 32-lane quarters). A copy and the MMAs
+// that one thread issues behind it run in that order.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  // no swizzle; 8-row groups of 128 bytes, one 16-byte column
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1u) << 46);
+}
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+// Requests a box into L2 only: legal before the kernel's dependency is met,
+// since a later write of it goes through L2 as well.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* tm, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 }  // namespace q3vl
