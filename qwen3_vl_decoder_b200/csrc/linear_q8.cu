@@ -7,10 +7,13 @@
 // one scale byte per operand row and 32 columns, here the same byte for the
 // four steps of a 128-column block). The partial sums of one output therefore
 // stay in one fp32 accumulator over the whole of K, and splitting K needs no
-// more than an addition. A warp builds the scale words of each k-block in the
-// layout the tensor core reads (q8.cuh), next to the operand tiles that TMA
-// brings (128-byte swizzle, 128 columns a box); the MMA thread copies them to
-// TMEM in front of the block's four MMAs.
+// more than an addition. TMA brings the operand tiles (128-byte swizzle, 128
+// columns a box); a warp builds the scale words in the layout that the tensor
+// core reads (q8.cuh), each with the bytes of four k-blocks, and the MMA
+// thread copies them to TMEM once per four k-blocks. (A word per k-block, the
+// first form, cost 200 against XXX us at 4096 x 2560 x 19456: the copies hold
+// up the MMAs behind them.)
+#include <cstdlib>
 #include "q3vl_internal.h"
 #include "q8.cuh"
 
@@ -18,13 +21,15 @@ namespace q3vl {
 namespace {
 
 constexpr int kKB = 128;                // k-block: bytes of K per stage and scale
-constexpr int kScaleBytes = 512;        // scale words of 128 rows
+constexpr int kScaleBytes = 512;        // scale words of 128 rows, four k-blocks
+constexpr int kSG = 4;                  // k-blocks per scale word
 
 struct LinQ8Params {
   int64_t M, N;
   int kblk;                // k-blocks: ceil(K / 128)
   const uint8_t* xs;       // [M][kblk]
   const uint8_t* ws;       // [ceil(N / 128)][kblk]
+  bool words;              // rows of xs and ws are whole, aligned 32-bit words
   const void* resid;       // [M][N] or null
   void* out;               // [M][N]
   int32_t* err;
@@ -40,10 +45,10 @@ __device__ __forceinline__ void add4(const float* r, float (&v)[4]) {
   v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
 }
 __device__ __forceinline__ void put4(__nv_bfloat16* o, const float (&v)[4]) {
-  *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  __stcs(reinterpret_cast<uint2*>(o), make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
 }
 __device__ __forceinline__ void put4(float* o, const float (&v)[4]) {
-  *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+  __stcs(reinterpret_cast<float4*>(o), make_float4(v[0], v[1], v[2], v[3]));
 }
 
 // Four neighbouring columns n .. n + 3 of output row m (n a multiple of 4):
@@ -66,6 +71,19 @@ __device__ __forceinline__ void finish4(const LinQ8Params& p, int64_t m, int64_t
         o[i] = static_cast<T>(v[i] + (p.resid != nullptr ? static_cast<float>(r[i]) : 0.f));
   }
 }
+
+// Scale bytes k .. k + 3 of a row of `end` bytes as one word (the last byte
+// repeated behind the end). `words`: rows are whole, aligned words, as for
+// every K that is a multiple of 512; else four loads, which cost the warp that
+// makes the words four times the load instructions.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int k, int end, bool words) {
+  if (words && k + kSG <= end) return __ldg(reinterpret_cast<const uint32_t*>(row + k));
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < kSG; ++i) w |= uint32_t(__ldg(row + min(k + i, end - 1))) << (8 * i);
+  return w;
+}
+constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // 2^0
 
 // ---------------------------------------------------------------------------
 // Few rows: the weight is the MMA's M operand (128 rows a tile) and a tile of
@@ -97,10 +115,12 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
   const int sfb = (sc.NB + 127) / 128;                            // scale copies of the x tile
   uint8_t* smA = smem;
   uint8_t* smB = smA + size_t(S) * kABytes;
-  uint8_t* smS = smB + size_t(S) * b_bytes;                       // [S][1 + sfb][512]
-  uint64_t* full = reinterpret_cast<uint64_t*>(smS + size_t(S) * (1 + sfb) * kScaleBytes);
+  uint8_t* smS = smB + size_t(S) * b_bytes;                       // [2][1 + sfb][512]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smS + size_t(2) * (1 + sfb) * kScaleBytes);
   uint64_t* empty = full + S;
-  uint64_t* acc_full = empty + S;
+  uint64_t* sfull = empty + S;
+  uint64_t* sempty = sfull + 2;
+  uint64_t* acc_full = sempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -113,8 +133,8 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
   const int64_t m0 = int64_t(tt) * sc.NB;
 
   if (threadIdx.x == 0) {
-    // full: the TMA thread and the scale warp; its loads count as bytes
-    for (int s = 0; s < S; ++s) { mbar_init(full + s, 2); mbar_init(empty + s, 1); }
+    for (int s = 0; s < S; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, 1); }
+    for (int s = 0; s < 2; ++s) { mbar_init(sfull + s, 1); mbar_init(sempty + s, 1); }
     mbar_init(acc_full, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -132,95 +152,106 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
   griddep_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
-      const int32_t row0 = tile * 128;
-      const int pre = n < S ? n : S;
-      // the weights may be asked for ahead of the dependency, as far as L2
+    const int32_t row0 = tile * 128;
+    const int pre = n < S ? n : S;
+    // the weights may be asked for ahead of the dependency, as far as L2
+    if (elect_one())
       for (int i = 0; i < pre; ++i) tma_prefetch_2d(&tmW, (k_lo + i) * kKB, row0);
-      griddep_wait();
-      int issued = 0;
-      for (int i = 0; i < n; ++i) {
-        const int s = i % S;
-        if (i >= S && !mbar_wait(empty + s, ((i / S) - 1) & 1, p.err, kWhereLinearQ8, abort_flag))
-          break;
+    griddep_wait();
+    int issued = 0, s = 0;
+    uint32_t ph = 1;
+    for (int i = 0; i < n; ++i) {
+      if (!mbar_wait(empty + s, ph, p.err, kWhereLinearQ8, abort_flag)) break;
+      if (elect_one()) {
         mbar_arrive_expect_tx(full + s, kABytes + b_bytes);
         tma_load_2d(smA + size_t(s) * kABytes, &tmW, full + s, (k_lo + i) * kKB, row0);
         tma_load_2d(smB + size_t(s) * b_bytes, &tmX, full + s, (k_lo + i) * kKB,
                     static_cast<int32_t>(m0));
-        issued = i + 1;
       }
-      // every issued load lands before the CTA may exit
-      for (int i = issued - S > 0 ? issued - S : 0; i < issued; ++i)
-        mbar_wait(full + (i % S), (i / S) & 1, p.err, kWhereLinearQ8, nullptr);
+      __syncwarp();
+      issued = i + 1;
+      if (++s == S) { s = 0; ph ^= 1; }
     }
+    // every issued load lands before the CTA may exit
+    for (int i = issued - S > 0 ? issued - S : 0; i < issued; ++i)
+      mbar_wait(full + (i % S), (i / S) & 1, p.err, kWhereLinearQ8, nullptr);
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_mxf8(128, sc.NB);
-      bool ok = true;
-      for (int i = 0; i < n; ++i) {
-        const int s = i % S;
-        if (!mbar_wait(full + s, (i / S) & 1, p.err, kWhereLinearQ8, abort_flag)) {
-          ok = false;
-          break;
+    const uint32_t idesc = idesc_mxf8(128, sc.NB);
+    bool ok = true;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < n; ++i) {
+      const int g = i / kSG;
+      const bool fresh = i % kSG == 0;
+      // two sets of scale columns in turn, behind the accumulator
+      const uint32_t sfa = tmem_base + sc.NB + (g & 1) * 4 * (1 + sfb), sfx = sfa + 4;
+      ok = !fresh || mbar_wait(sfull + (g & 1), (g >> 1) & 1, p.err, kWhereLinearQ8, abort_flag);
+      ok = ok && mbar_wait(full + s, ph, p.err, kWhereLinearQ8, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t da = sdesc_sw128(smem_u32(smA + size_t(s) * kABytes), 16, 1024);
+      const uint64_t db = sdesc_sw128(smem_u32(smB + size_t(s) * b_bytes), 16, 1024);
+      const uint64_t ds = sdesc_scales(smem_u32(smS + size_t(g & 1) * (1 + sfb) * kScaleBytes));
+      const uint32_t id = idesc | idesc_sf(i % kSG);
+      if (elect_one()) {
+        if (fresh) {
+          tmem_cp_scales(sfa, ds);
+          for (int c = 1; c <= sfb; ++c) tmem_cp_scales(sfa + 4 * c, ds + c * (kScaleBytes / 16));
+          umma_commit(sempty + (g & 1));
         }
-        tc_fence_after();
-        // two sets of scale columns in turn, behind the accumulator
-        const uint32_t sfa = tmem_base + sc.NB + (i & 1) * 4 * (1 + sfb), sfx = sfa + 4;
-        const uint32_t sw = smem_u32(smS + size_t(s) * (1 + sfb) * kScaleBytes);
-        tmem_cp_scales(sfa, sdesc_scales(sw));
-        for (int c = 0; c < sfb; ++c)
-          tmem_cp_scales(sfx + 4 * c, sdesc_scales(sw + (1 + c) * kScaleBytes));
-        const uint32_t a0 = smem_u32(smA + size_t(s) * kABytes);
-        const uint32_t b0 = smem_u32(smB + size_t(s) * b_bytes);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_mxf8_ss(tmem_base, sdesc_sw128(a0 + kk * 32, 16, 1024),
-                       sdesc_sw128(b0 + kk * 32, 16, 1024), idesc, sfa, sfx,
-                       (i | kk) != 0 ? 1u : 0u);
+          umma_mxf8_ss(tmem_base, da + 2 * kk, db + 2 * kk, id, sfa, sfx, (i | kk) != 0 ? 1u : 0u);
         umma_commit(empty + s);
+        if (i == n - 1) umma_commit(acc_full);
       }
-      if (ok) umma_commit(acc_full);
-      else *abort_flag = 1;
+      __syncwarp();
+      if (++s == S) { s = 0; ph ^= 1; }
     }
-    __syncwarp();
+    if (!ok) *abort_flag = 1;
   } else {
     griddep_wait();
     if (warp == 2) {
-      // scale words of every k-block: one byte for the weight tile, one per
-      // row of x (rows past M are zero: any scale)
-      uint32_t nx[7], nw;
-      auto load = [&](int i) {
-        nw = p.ws[int64_t(tile) * p.kblk + k_lo + i];
+      // Scale words: the bytes of four k-blocks for the weight tile and for
+      // each row of x (rows past M are zero: any scale), requested one group
+      // ahead of the one being written.
+      const int groups = (n + kSG - 1) / kSG;
+      uint32_t x[7], w, nx[7], nw;
+      const bool words = p.words && k_lo % kSG == 0;
+      auto request = [&](int g) {
+        const int k = k_lo + g * kSG, end = k_lo + n;
+        nw = scale_word(p.ws + int64_t(tile) * p.kblk, k, end, words);
 #pragma unroll
         for (int j = 0; j < 7; ++j) {
           const int r = lane + 32 * j;
-          nx[j] = r < sc.NB && m0 + r < p.M ? p.xs[(m0 + r) * p.kblk + k_lo + i] : 127u;
+          nx[j] = r < sc.NB && m0 + r < p.M
+                      ? scale_word(p.xs + (m0 + r) * p.kblk, k, end, words) : kNoScale;
         }
       };
-      if (n > 0) load(0);
-      for (int i = 0; i < n; ++i) {
-        const int s = i % S;
+      request(0);
+      for (int g = 0; g < groups; ++g) {
+        w = nw;
+#pragma unroll
+        for (int j = 0; j < 7; ++j) x[j] = nx[j];
         bool ok = true;
-        if (i >= S) {
+        if (g >= 2) {
           if (lane == 0)
-            ok = mbar_wait(empty + s, ((i / S) - 1) & 1, p.err, kWhereLinearQ8, abort_flag);
+            ok = mbar_wait(sempty + (g & 1), ((g >> 1) - 1) & 1, p.err, kWhereLinearQ8, abort_flag);
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
         if (!ok) break;
-        uint8_t* w = smS + size_t(s) * (1 + sfb) * kScaleBytes + lane * 16;
-        const uint32_t a = nw * 0x01010101u;
-        *reinterpret_cast<uint4*>(w) = make_uint4(a, a, a, a);
-        *reinterpret_cast<uint4*>(w + kScaleBytes) =
-            make_uint4(nx[0] * 0x01010101u, nx[1] * 0x01010101u, nx[2] * 0x01010101u,
-                       nx[3] * 0x01010101u);
+        uint8_t* dst = smS + size_t(g & 1) * (1 + sfb) * kScaleBytes + lane * 16;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w, w, w, w);
+        *reinterpret_cast<uint4*>(dst + kScaleBytes) = make_uint4(x[0], x[1], x[2], x[3]);
         if (sfb > 1)
-          *reinterpret_cast<uint4*>(w + 2 * kScaleBytes) =
-              make_uint4(nx[4] * 0x01010101u, nx[5] * 0x01010101u, nx[6] * 0x01010101u,
-                         127u * 0x01010101u);
+          *reinterpret_cast<uint4*>(dst + 2 * kScaleBytes) = make_uint4(x[4], x[5], x[6], 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full + s);
-        if (i + 1 < n) load(i + 1);
+        if (lane == 0) mbar_arrive(sfull + (g & 1));
+        if (g + 1 < groups) request(g + 1);  // behind the fence, which would wait for it
       }
     }
     __syncwarp();
@@ -291,6 +322,301 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows: x is the M operand of a CTA pair (tcgen05.mma cta_group::2, a
+// 256 x BN tile, each CTA staging its 128 rows of x and BN / 2 rows of the
+// weight per k-block), persistent over tiles, bound by the tensor cores. Two
+// accumulators let the epilogue of a tile overlap the next tile's products;
+// TMEM holds them and two sets of scale columns (of one CTA: 128 rows of x and
+// the tile's BN weight rows), so BN is at most 224, not 256. One warp of each
+// CTA builds the scale words of its half in step with the loads.
+// ---------------------------------------------------------------------------
+constexpr int kPairThreads = 256;       // warp 0 TMA, 1 MMA, 2-5 epilogue, 6-7 scales
+constexpr int kEpiLd = 36;              // floats per row of a warp's 32 x 32 staging block
+
+template <int BN>
+struct PairCfg {
+  static constexpr int kABytes = 128 * kKB;
+  static constexpr int kBBytes = BN / 2 * kKB;
+  static constexpr int kStages = 6;
+  static constexpr int kScales = 3 * kScaleBytes;  // x rows; weight rows 0-127, 128-255
+  static constexpr int kSlots = 4;                 // of scale words, two for each of its warps
+  static constexpr int kEpi = 4 * 32 * kEpiLd * 4;
+  static constexpr int kAcc = (BN + 31) / 32 * 32;
+  static constexpr int kSfCol = 2 * kAcc;          // two sets of 12 columns
+  static constexpr size_t kSmem =
+      1024 + size_t(kStages) * (kABytes + kBBytes) + size_t(kSlots) * kScales + kEpi + 256;
+  static_assert(BN % 32 == 0 && kBBytes % 1024 == 0, "MMA and swizzle");
+  static_assert(kSfCol + 24 <= 512, "TMEM columns");
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+template <typename T, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+linear_q8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
+                      const __grid_constant__ CUtensorMap tmW, LinQ8Params p, int tiles_m,
+                      int tiles) {
+  using C = PairCfg<BN>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* smA = smem;
+  uint8_t* smB = smA + S * C::kABytes;
+  uint8_t* smS = smB + S * C::kBBytes;
+  float* smE = reinterpret_cast<float*>(smS + C::kSlots * C::kScales);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(smE) + C::kEpi);
+  uint64_t* empty = full + S;
+  uint64_t* sfull = empty + S;
+  uint64_t* sempty = sfull + C::kSlots;
+  uint64_t* tfull = sempty + C::kSlots;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool lead = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  if (threadIdx.x == 0) {
+    // of the even CTA, full: its TMA thread, whose bytes count both CTAs'
+    // loads; sfull: both scale warps; tempty: both CTAs' four epilogue warps
+    for (int s = 0; s < S; ++s) { mbar_init(full + s, 1); mbar_init(empty + s, 1); }
+    for (int s = 0; s < C::kSlots; ++s) { mbar_init(sfull + s, 2); mbar_init(sempty + s, 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(tfull + b, 1); mbar_init(tempty + b, 8); }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    griddep_wait();
+    int stage = 0;
+    uint32_t ph = 0, issued = 0, last_ph = 0;  // the latter two: a bit per stage
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const int32_t m0 = (t % tiles_m) * 256 + static_cast<int32_t>(rank) * 128;
+      const int32_t n0 = (t / tiles_m) * BN + static_cast<int32_t>(rank) * (BN / 2);
+      for (int kb = 0; kb < p.kblk; ++kb) {
+        ok = mbar_wait<true>(empty + stage, ph ^ 1, p.err, kWhereLinearQ8, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t fb = map_to_cta(smem_u32(full + stage), 0);
+          if (lead) mbar_arrive_expect_tx(full + stage, 2 * (C::kABytes + C::kBBytes));
+          tma_load_2d_pair(smA + stage * C::kABytes, &tmX, fb, kb * kKB, m0);
+          tma_load_2d_pair(smB + stage * C::kBBytes, &tmW, fb, kb * kKB, n0);
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        last_ph = (last_ph & ~(1u << stage)) | (ph << stage);
+        if (++stage == S) { stage = 0; ph ^= 1; }
+      }
+    }
+    // every issued load lands before the pair exits (the even CTA's barrier
+    // counts both CTAs' bytes; the last cluster barrier holds the odd CTA)
+    if (lead)
+      for (int s = 0; s < S; ++s)
+        if (issued & (1u << s))
+          mbar_wait<true>(full + s, (last_ph >> s) & 1u, p.err, kWhereLinearQ8, nullptr);
+  } else if (warp == 1) {
+    if (lead) {
+      constexpr uint32_t idesc = idesc_mxf8(256, BN);
+      int stage = 0, it = 0, slot = 0, set = 1;
+      uint32_t ph = 0, sph = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs, ++it) {
+        const int buf = it & 1;
+        ok = mbar_wait<true>(tempty + buf, ((it >> 1) & 1) ^ 1, p.err, kWhereLinearQ8, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * C::kAcc;
+        for (int kb = 0; kb < p.kblk; ++kb) {
+          const bool fresh = kb % kSG == 0;
+          ok = !fresh || mbar_wait<true>(sfull + slot, sph, p.err, kWhereLinearQ8, abort_flag);
+          ok = ok && mbar_wait<true>(full + stage, ph, p.err, kWhereLinearQ8, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (fresh) set ^= 1;
+          const uint32_t sfx = tmem_base + C::kSfCol + set * 12, sfw = sfx + 4;
+          const uint64_t da = sdesc_sw128(smem_u32(smA + stage * C::kABytes), 16, 1024);
+          const uint64_t db = sdesc_sw128(smem_u32(smB + stage * C::kBBytes), 16, 1024);
+          const uint64_t ds = sdesc_scales(smem_u32(smS + slot * C::kScales));
+          const uint32_t id = idesc | idesc_sf(kb % kSG);
+          if (elect_one()) {
+            if (fresh) {
+              tmem_cp_scales_pair(sfx, ds);
+              tmem_cp_scales_pair(sfw, ds + kScaleBytes / 16);
+              if (BN > 128) tmem_cp_scales_pair(sfw + 4, ds + 2 * (kScaleBytes / 16));
+              umma_commit_pair(sempty + slot, 0x3);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_mxf8_ss_pair(d, da + 2 * k, db + 2 * k, id, sfx, sfw, (kb | k) != 0 ? 1u : 0u);
+            umma_commit_pair(empty + stage, 0x3);
+            if (kb == p.kblk - 1) umma_commit_pair(tfull + buf, 0x3);
+          }
+          __syncwarp();
+          if (fresh && ++slot == C::kSlots) { slot = 0; sph ^= 1; }
+          if (++stage == S) { stage = 0; ph ^= 1; }
+        }
+      }
+      // all issued MMAs complete before either CTA releases its TMEM
+      if (elect_one()) umma_commit_pair(drain, 0x3);
+      __syncwarp();
+    }
+    mbar_wait<true>(drain, 0, p.err, kWhereLinearQ8, nullptr);
+  } else if (warp >= 6) {
+    griddep_wait();
+    // Scale words: the bytes of four k-blocks for each row of x (lane's rows
+    // lane + 32 j; rows past M are zero: any scale) and each weight row, whose
+    // tile touches up to three 128-row blocks. The two warps take the groups
+    // of four k-blocks in turn: one group (0.9 us of MMAs) is not much more
+    // than the latency of its loads and of the proxy fence.
+    const int half = warp - 6;
+    int slot = half;
+    uint32_t ph = 0;
+    bool ok = true;
+    const int wblks = static_cast<int>((p.N + 127) / 128), groups = (p.kblk + kSG - 1) / kSG;
+    uint32_t nx[4], nw[3];
+    auto request = [&](int t, int g) {
+      const int64_t m0 = int64_t(t % tiles_m) * 256 + rank * 128;
+      const int w0 = (t / tiles_m) * BN / 128;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t r = m0 + lane + 32 * j;
+        nx[j] = r < p.M ? scale_word(p.xs + r * p.kblk, g * kSG, p.kblk, p.words) : kNoScale;
+      }
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        nw[j] = scale_word(p.ws + int64_t(min(w0 + j, wblks - 1)) * p.kblk, g * kSG, p.kblk,
+                           p.words);
+    };
+    // this warp's groups: every second one of the sequence over all tiles
+    int t = pair, g = half;
+    auto settle = [&]() {
+      while (g >= groups && t < tiles) { g -= groups; t += pairs; }
+    };
+    settle();
+    if (t < tiles) request(t, g);
+    while (t < tiles) {
+      const int n0 = (t / tiles_m) * BN, w0 = n0 / 128;
+      uint32_t x[4], w[3], u[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = nx[j];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) w[j] = nw[j];
+      if (lane == 0)
+        ok = mbar_wait<true>(sempty + slot, ph ^ 1, p.err, kWhereLinearQ8, abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      uint8_t* dst = smS + slot * C::kScales + lane * 16;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int b = (n0 + lane + 32 * j) / 128 - w0;  // 0 .. 2
+        u[j] = b == 0 ? w[0] : b == 1 ? w[1] : w[2];
+      }
+      *reinterpret_cast<uint4*>(dst + kScaleBytes) = make_uint4(u[0], u[1], u[2], u[3]);
+      if (BN > 128)
+        *reinterpret_cast<uint4*>(dst + 2 * kScaleBytes) = make_uint4(u[4], u[5], u[6], u[7]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_peer(map_to_cta(smem_u32(sfull + slot), 0));
+      slot ^= 2;
+      if (slot == half) ph ^= 1;
+      g += 2;
+      settle();
+      if (t < tiles) request(t, g);  // behind the fence, which would wait for it
+    }
+    __syncwarp();
+  } else {
+    griddep_wait();
+    const int q = warp & 3;
+    float* se = smE + (warp - 2) * 32 * kEpiLd;
+    const uint32_t lane_field = static_cast<uint32_t>(32 * q) << 16;
+    const uint32_t tempty_lead = map_to_cta(smem_u32(tempty), 0);
+    int it = 0;
+    for (int t = pair; t < tiles; t += pairs, ++it) {
+      const int buf = it & 1;
+      const int64_t m0 = int64_t(t % tiles_m) * 256 + rank * 128 + 32 * q;
+      const int64_t n0 = int64_t(t / tiles_m) * BN;
+      bool ok = true;
+      if (lane == 0)
+        ok = mbar_wait<true>(tfull + buf, (it >> 1) & 1, p.err, kWhereLinearQ8, abort_flag);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + buf * C::kAcc + lane_field;
+#pragma unroll 1
+      for (int cc = 0; cc < BN / 32; ++cc) {
+        uint32_t u[32];
+        tmem_ld32(tb + 32 * cc, u);
+        tmem_ld_wait();
+        if (cc == BN / 32 - 1) {  // the accumulator is read: hand it back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_peer(tempty_lead + buf * sizeof(uint64_t));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(se + lane * kEpiLd + 4 * j) =
+              make_float4(__uint_as_float(u[4 * j]), __uint_as_float(u[4 * j + 1]),
+                          __uint_as_float(u[4 * j + 2]), __uint_as_float(u[4 * j + 3]));
+        __syncwarp();
+        // eight lanes to a row: whole sectors of each row leave together
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const float4 f =
+              *reinterpret_cast<const float4*>(se + r * kEpiLd + 4 * (lane & 7));
+          float v[4] = {f.x, f.y, f.z, f.w};
+          if (m0 + r < p.M) finish4<T>(p, m0 + r, n0 + 32 * cc + 4 * (lane & 7), v);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // no CTA of the pair leaves while the other may touch its memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+template <typename T, int BN>
+cudaError_t launch_pair(const uint8_t* xq, int64_t M, const uint8_t* wq, int64_t N, int64_t K,
+                        const LinQ8Params& p, cudaStream_t st) {
+  using C = PairCfg<BN>;
+  CUtensorMap tmX, tmW;
+  if (!make_tmap_u8(&tmX, xq, M, K, K, kKB, 128) || !make_tmap_u8(&tmW, wq, N, K, K, kKB, BN / 2))
+    return cudaErrorInvalidValue;
+  const int64_t tiles_m = (M + 255) / 256, tiles = tiles_m * ((N + BN - 1) / BN);
+  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+  auto kern = linear_q8_pair_kernel<T, BN>;
+  cudaError_t e = smem_attr_at_least(reinterpret_cast<const void*>(kern), C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = tiles < sm_count() / 2 ? tiles : sm_count() / 2;
+  e = launch_pdl_plain(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kPairThreads), C::kSmem,
+                       st, tmX, tmW, p, static_cast<int>(tiles_m), static_cast<int>(tiles));
+  if (e != cudaSuccess) return e;
+  return counted_launch(1);
+}
+
 SkSched sk_sched(int64_t M, int64_t N, int64_t K) {
   SkSched s;
   s.ttiles = static_cast<int>((M + kSkMaxNB - 1) / kSkMaxNB);
@@ -298,11 +624,12 @@ SkSched sk_sched(int64_t M, int64_t N, int64_t K) {
   s.tiles = static_cast<int>((N + 127) / 128);
   const int kblk = static_cast<int>((K + kKB - 1) / kKB);
   const int sfb = (s.NB + 127) / 128;
-  const size_t stage = size_t(128) * kKB + size_t(s.NB) * kKB + size_t(1 + sfb) * kScaleBytes;
-  int st = static_cast<int>(size_t(110 * 1024) / stage);  // two CTAs share an SM
+  const size_t stage = size_t(128) * kKB + size_t(s.NB) * kKB;
+  int st = static_cast<int>(size_t(108 * 1024) / stage);  // two CTAs share an SM
   s.stages = st < 2 ? 2 : (st > 6 ? 6 : st);
   if (s.stages > kblk) s.stages = kblk < 2 ? 2 : kblk;
-  s.smem = 1024 + size_t(s.stages) * stage + size_t(2 * s.stages + 1) * 8 + 16;
+  s.smem = 1024 + size_t(s.stages) * stage + size_t(2 * (1 + sfb)) * kScaleBytes +
+           size_t(2 * s.stages + 5) * 8 + 16;
   while (s.tcols < static_cast<uint32_t>(s.NB + 8 * (1 + sfb))) s.tcols <<= 1;
   const int64_t work = int64_t(s.tiles) * s.ttiles;
   int64_t splits = 2 * int64_t(sm_count()) / work;
@@ -342,9 +669,15 @@ cudaError_t launch_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, co
   p.M = M; p.N = N;
   p.kblk = static_cast<int>((K + kKB - 1) / kKB);
   p.xs = xs; p.ws = ws; p.resid = resid; p.out = out;
+  p.words = p.kblk % kSG == 0 && reinterpret_cast<uintptr_t>(xs) % 4 == 0 &&
+            reinterpret_cast<uintptr_t>(ws) % 4 == 0;
   p.err = device_error_ptr();
-  if (out_bf16) return launch_rows<__nv_bfloat16>(xq, M, wq, N, K, p, st);
-  return launch_rows<float>(xq, M, wq, N, K, p, st);
+  const char* f8 = getenv("Q8F");
+  if (f8 ? f8[0] == 'r' : M <= 224)
+    return out_bf16 ? launch_rows<__nv_bfloat16>(xq, M, wq, N, K, p, st)
+                    : launch_rows<float>(xq, M, wq, N, K, p, st);
+  return out_bf16 ? launch_pair<__nv_bfloat16, 224>(xq, M, wq, N, K, p, st)
+                  : launch_pair<float, 224>(xq, M, wq, N, K, p, st);
 }
 
 }  // namespace q3vl
