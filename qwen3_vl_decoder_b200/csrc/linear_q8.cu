@@ -11,9 +11,8 @@
 // columns a box); a warp builds the scale words in the layout that the tensor
 // core reads (q8.cuh), each with the bytes of four k-blocks, and the MMA
 // thread copies them to TMEM once per four k-blocks. (A word per k-block, the
-// first form, cost 200 against XXX us at 4096 x 2560 x 19456: the copies hold
+// first form, cost 200 against 187 us at 4096 x 2560 x 19456: the copies hold
 // up the MMAs behind them.)
-#include <cstdlib>
 #include "q3vl_internal.h"
 #include "q8.cuh"
 
@@ -49,6 +48,57 @@ __device__ __forceinline__ void put4(__nv_bfloat16* o, const float (&v)[4]) {
 }
 __device__ __forceinline__ void put4(float* o, const float (&v)[4]) {
   __stcs(reinterpret_cast<float4*>(o), make_float4(v[0], v[1], v[2], v[3]));
+}
+
+// 32 bytes of a row (32-byte aligned): a whole sector from one thread.
+__device__ __forceinline__ void put32(void* o, const uint32_t (&w)[8]) {
+  asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void get32(const void* i, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(i)
+               : "memory");
+}
+
+// 32 columns of one output row from n (a multiple of 32), for rows whose
+// 32-byte units are whole and aligned.
+__device__ __forceinline__ void finish_wide(const LinQ8Params& p, int64_t m, int64_t n,
+                                            const float (&v)[32], __nv_bfloat16*) {
+  const int64_t at = m * p.N + n;
+#pragma unroll
+  for (int i = 0; i < 32; i += 16) {
+    if (n + i >= p.N) return;
+    uint32_t w[8], r[8];
+    if (p.resid != nullptr) get32(static_cast<const __nv_bfloat16*>(p.resid) + at + i, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float2 f = make_float2(v[i + 2 * j], v[i + 2 * j + 1]);
+      if (p.resid != nullptr) {
+        const float2 q = unpack_bf16x2(r[j]);
+        f.x += q.x; f.y += q.y;
+      }
+      w[j] = pack_bf16x2(f.x, f.y);
+    }
+    put32(static_cast<__nv_bfloat16*>(p.out) + at + i, w);
+  }
+}
+__device__ __forceinline__ void finish_wide(const LinQ8Params& p, int64_t m, int64_t n,
+                                            const float (&v)[32], float*) {
+  const int64_t at = m * p.N + n;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    if (n + i >= p.N) return;
+    uint32_t w[8], r[8];
+    if (p.resid != nullptr) get32(static_cast<const float*>(p.resid) + at + i, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = __float_as_uint(v[i + j] + (p.resid != nullptr ? __uint_as_float(r[j]) : 0.f));
+    put32(static_cast<float*>(p.out) + at + i, w);
+  }
 }
 
 // Four neighbouring columns n .. n + 3 of output row m (n a multiple of 4):
@@ -87,7 +137,7 @@ constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // 2^0
 
 // ---------------------------------------------------------------------------
 // Few rows: the weight is the MMA's M operand (128 rows a tile) and a tile of
-// NB <= 224 rows of x its N operand, so that one decoded token pads N to 16
+// NB <= 128 rows of x its N operand, so that one decoded token pads N to 16
 // and not M to 128. Bound by the weight's bytes; K is split over up to 8 CTAs
 // of a cluster (about two CTAs per SM stream weights), which leave their fp32
 // partial tiles in shared memory and share out the rows of x to add them up
@@ -95,7 +145,8 @@ constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // 2^0
 // ---------------------------------------------------------------------------
 constexpr int kSkThreads = 192;         // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue, 2 scales first
 constexpr int kSkMaxSplits = 8;         // portable cluster size
-constexpr int kSkMaxNB = 224;           // with the scale words 248 TMEM columns: two CTAs per SM
+constexpr int kSkMaxNB = 128;           // scale words of one copy; 224 measured 24.8 against 16.9 us at
+                                        // 256 x 9728 x 2560: half the CTAs, a ring half as deep
 
 struct SkSched {
   int NB = 16, ttiles = 1, tiles = 1, splits = 1, stages = 2;
@@ -112,11 +163,10 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int S = sc.stages;
   const uint32_t b_bytes = static_cast<uint32_t>(sc.NB) * kKB;   // a multiple of 2 KB
-  const int sfb = (sc.NB + 127) / 128;                            // scale copies of the x tile
   uint8_t* smA = smem;
   uint8_t* smB = smA + size_t(S) * kABytes;
-  uint8_t* smS = smB + size_t(S) * b_bytes;                       // [2][1 + sfb][512]
-  uint64_t* full = reinterpret_cast<uint64_t*>(smS + size_t(2) * (1 + sfb) * kScaleBytes);
+  uint8_t* smS = smB + size_t(S) * b_bytes;                       // [2]: weight, x
+  uint64_t* full = reinterpret_cast<uint64_t*>(smS + 4 * kScaleBytes);
   uint64_t* empty = full + S;
   uint64_t* sfull = empty + S;
   uint64_t* sempty = sfull + 2;
@@ -184,7 +234,7 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
       const int g = i / kSG;
       const bool fresh = i % kSG == 0;
       // two sets of scale columns in turn, behind the accumulator
-      const uint32_t sfa = tmem_base + sc.NB + (g & 1) * 4 * (1 + sfb), sfx = sfa + 4;
+      const uint32_t sfa = tmem_base + sc.NB + (g & 1) * 8, sfx = sfa + 4;
       ok = !fresh || mbar_wait(sfull + (g & 1), (g >> 1) & 1, p.err, kWhereLinearQ8, abort_flag);
       ok = ok && mbar_wait(full + s, ph, p.err, kWhereLinearQ8, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -194,12 +244,12 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
       tc_fence_after();
       const uint64_t da = sdesc_sw128(smem_u32(smA + size_t(s) * kABytes), 16, 1024);
       const uint64_t db = sdesc_sw128(smem_u32(smB + size_t(s) * b_bytes), 16, 1024);
-      const uint64_t ds = sdesc_scales(smem_u32(smS + size_t(g & 1) * (1 + sfb) * kScaleBytes));
+      const uint64_t ds = sdesc_scales(smem_u32(smS + (g & 1) * 2 * kScaleBytes));
       const uint32_t id = idesc | idesc_sf(i % kSG);
       if (elect_one()) {
         if (fresh) {
           tmem_cp_scales(sfa, ds);
-          for (int c = 1; c <= sfb; ++c) tmem_cp_scales(sfa + 4 * c, ds + c * (kScaleBytes / 16));
+          tmem_cp_scales(sfx, ds + kScaleBytes / 16);
           umma_commit(sempty + (g & 1));
         }
 #pragma unroll
@@ -219,13 +269,13 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
       // each row of x (rows past M are zero: any scale), requested one group
       // ahead of the one being written.
       const int groups = (n + kSG - 1) / kSG;
-      uint32_t x[7], w, nx[7], nw;
+      uint32_t x[4], w, nx[4], nw;
       const bool words = p.words && k_lo % kSG == 0;
       auto request = [&](int g) {
         const int k = k_lo + g * kSG, end = k_lo + n;
         nw = scale_word(p.ws + int64_t(tile) * p.kblk, k, end, words);
 #pragma unroll
-        for (int j = 0; j < 7; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const int r = lane + 32 * j;
           nx[j] = r < sc.NB && m0 + r < p.M
                       ? scale_word(p.xs + (m0 + r) * p.kblk, k, end, words) : kNoScale;
@@ -235,7 +285,7 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
       for (int g = 0; g < groups; ++g) {
         w = nw;
 #pragma unroll
-        for (int j = 0; j < 7; ++j) x[j] = nx[j];
+        for (int j = 0; j < 4; ++j) x[j] = nx[j];
         bool ok = true;
         if (g >= 2) {
           if (lane == 0)
@@ -243,11 +293,9 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
         if (!ok) break;
-        uint8_t* dst = smS + size_t(g & 1) * (1 + sfb) * kScaleBytes + lane * 16;
+        uint8_t* dst = smS + (g & 1) * 2 * kScaleBytes + lane * 16;
         *reinterpret_cast<uint4*>(dst) = make_uint4(w, w, w, w);
         *reinterpret_cast<uint4*>(dst + kScaleBytes) = make_uint4(x[0], x[1], x[2], x[3]);
-        if (sfb > 1)
-          *reinterpret_cast<uint4*>(dst + 2 * kScaleBytes) = make_uint4(x[4], x[5], x[6], 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(sfull + (g & 1));
@@ -293,23 +341,29 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
     cluster_sync();  // every CTA's partials of this round are in its shared memory
     if (warp >= 2 && run) {
 #pragma unroll 1
-      for (int jj = split + (warp - 2) * sc.splits; jj < nj; jj += 4 * sc.splits) {
-        const uint32_t own = smem_u32(red + jj * 128 + 4 * lane);
-        // every split's values requested before any is added: one DSMEM round
-        // trip, then the sum in split order
-        float w[kSkMaxSplits][4];
+      for (int jj = split + (warp - 2) * sc.splits; jj < nj; jj += 8 * sc.splits) {
+        // two rows at a time, every split's values requested before any is
+        // added: one DSMEM round trip, then the sum in split order
+        const int j1 = jj + 4 * sc.splits;
+        float4 w[2][kSkMaxSplits];
 #pragma unroll
-        for (int sp = 0; sp < kSkMaxSplits; ++sp) {
-          const uint32_t ra = map_to_cta(own, static_cast<uint32_t>(sp < sc.splits ? sp : 0));
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t own = smem_u32(red + (i == 0 || j1 >= nj ? jj : j1) * 128 + 4 * lane);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[sp][i] = sp < sc.splits ? ld_dsmem_f32(ra + 4u * i) : 0.f;
+          for (int sp = 0; sp < kSkMaxSplits; ++sp)
+            if (sp < sc.splits) w[i][sp] = ld_dsmem_f32x4(map_to_cta(own, sp));
         }
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int sp = 0; sp < kSkMaxSplits; ++sp)
+        for (int i = 0; i < 2; ++i) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += w[sp][i];
-        finish4<T>(p, m0 + j0 + jj, int64_t(tile) * 128 + 4 * lane, v);
+          for (int sp = 0; sp < kSkMaxSplits; ++sp)
+            if (sp < sc.splits) {
+              v[0] += w[i][sp].x; v[1] += w[i][sp].y; v[2] += w[i][sp].z; v[3] += w[i][sp].w;
+            }
+          const int j = i == 0 ? jj : j1;
+          if (j < nj) finish4<T>(p, m0 + j0 + j, int64_t(tile) * 128 + 4 * lane, v);
+        }
       }
     }
     cluster_sync();  // no CTA overwrites or leaves its buffer while another may read it
@@ -328,20 +382,24 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
 // weight per k-block), persistent over tiles, bound by the tensor cores. Two
 // accumulators let the epilogue of a tile overlap the next tile's products;
 // TMEM holds them and two sets of scale columns (of one CTA: 128 rows of x and
-// the tile's BN weight rows), so BN is at most 224, not 256. One warp of each
-// CTA builds the scale words of its half in step with the loads.
+// the tile's BN weight rows), so BN is at most 224, not 256. Shared memory is
+// as busy as the tensor core (per k-block 30 KB written by TMA and 30 KB read by
+// the MMAs in 448 cycles of 128 bytes), so the epilogue stays out of it where
+// rows allow: each thread stores whole 32-byte sectors of its own row. Measured
+// at 4096 x 2560 x 19456: 150 us (2700 TFLOP/s), 168 with the stores coalesced
+// through shared memory in fp32, 155 with TMA stores of rounded boxes.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 256;       // warp 0 TMA, 1 MMA, 2-5 epilogue, 6-7 scales
 constexpr int kEpiLd = 36;              // floats per row of a warp's 32 x 32 staging block
 
-template <int BN>
+template <int BN, bool WIDE>
 struct PairCfg {
   static constexpr int kABytes = 128 * kKB;
   static constexpr int kBBytes = BN / 2 * kKB;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = 6;                // 7 measured no faster
   static constexpr int kScales = 3 * kScaleBytes;  // x rows; weight rows 0-127, 128-255
   static constexpr int kSlots = 4;                 // of scale words, two for each of its warps
-  static constexpr int kEpi = 4 * 32 * kEpiLd * 4;
+  static constexpr int kEpi = WIDE ? 0 : 4 * 32 * kEpiLd * 4;
   static constexpr int kAcc = (BN + 31) / 32 * 32;
   static constexpr int kSfCol = 2 * kAcc;          // two sets of 12 columns
   static constexpr size_t kSmem =
@@ -351,12 +409,12 @@ struct PairCfg {
   static_assert(kSmem <= 232448, "shared memory");
 };
 
-template <typename T, int BN>
+template <typename T, int BN, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 linear_q8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
                       const __grid_constant__ CUtensorMap tmW, LinQ8Params p, int tiles_m,
                       int tiles) {
-  using C = PairCfg<BN>;
+  using C = PairCfg<BN, WIDE>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -571,22 +629,32 @@ linear_q8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
           __syncwarp();
           if (lane == 0) mbar_arrive_peer(tempty_lead + buf * sizeof(uint64_t));
         }
+        if constexpr (WIDE) {
+          float v[32];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(se + lane * kEpiLd + 4 * j) =
-              make_float4(__uint_as_float(u[4 * j]), __uint_as_float(u[4 * j + 1]),
-                          __uint_as_float(u[4 * j + 2]), __uint_as_float(u[4 * j + 3]));
-        __syncwarp();
-        // eight lanes to a row: whole sectors of each row leave together
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+          if (m0 + lane < p.M)
+            finish_wide(p, m0 + lane, n0 + 32 * cc, v, static_cast<T*>(nullptr));
+        } else {
+          // through shared memory, so that a row's 32 columns leave together
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3);
-          const float4 f =
-              *reinterpret_cast<const float4*>(se + r * kEpiLd + 4 * (lane & 7));
-          float v[4] = {f.x, f.y, f.z, f.w};
-          if (m0 + r < p.M) finish4<T>(p, m0 + r, n0 + 32 * cc + 4 * (lane & 7), v);
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(se + lane * kEpiLd + 4 * j) =
+                make_float4(__uint_as_float(u[4 * j]), __uint_as_float(u[4 * j + 1]),
+                            __uint_as_float(u[4 * j + 2]), __uint_as_float(u[4 * j + 3]));
+          __syncwarp();
+          const int64_t n = n0 + 32 * cc + lane;
+          const int rows = static_cast<int>(p.M - m0 < 32 ? p.M - m0 : 32);
+          if (n < p.N)
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r) {
+              const int64_t at = (m0 + r) * p.N + n;
+              float v = se[r * kEpiLd + lane];
+              if (p.resid != nullptr) v += static_cast<float>(static_cast<const T*>(p.resid)[at]);
+              static_cast<T*>(p.out)[at] = static_cast<T>(v);
+            }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
   }
@@ -598,16 +666,16 @@ linear_q8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
   }
 }
 
-template <typename T, int BN>
+template <typename T, int BN, bool WIDE>
 cudaError_t launch_pair(const uint8_t* xq, int64_t M, const uint8_t* wq, int64_t N, int64_t K,
                         const LinQ8Params& p, cudaStream_t st) {
-  using C = PairCfg<BN>;
+  using C = PairCfg<BN, WIDE>;
   CUtensorMap tmX, tmW;
   if (!make_tmap_u8(&tmX, xq, M, K, K, kKB, 128) || !make_tmap_u8(&tmW, wq, N, K, K, kKB, BN / 2))
     return cudaErrorInvalidValue;
   const int64_t tiles_m = (M + 255) / 256, tiles = tiles_m * ((N + BN - 1) / BN);
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
-  auto kern = linear_q8_pair_kernel<T, BN>;
+  auto kern = linear_q8_pair_kernel<T, BN, WIDE>;
   cudaError_t e = smem_attr_at_least(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t pairs = tiles < sm_count() / 2 ? tiles : sm_count() / 2;
@@ -623,14 +691,8 @@ SkSched sk_sched(int64_t M, int64_t N, int64_t K) {
   s.NB = static_cast<int>(((M + s.ttiles - 1) / s.ttiles + 15) / 16 * 16);
   s.tiles = static_cast<int>((N + 127) / 128);
   const int kblk = static_cast<int>((K + kKB - 1) / kKB);
-  const int sfb = (s.NB + 127) / 128;
   const size_t stage = size_t(128) * kKB + size_t(s.NB) * kKB;
-  int st = static_cast<int>(size_t(108 * 1024) / stage);  // two CTAs share an SM
-  s.stages = st < 2 ? 2 : (st > 6 ? 6 : st);
-  if (s.stages > kblk) s.stages = kblk < 2 ? 2 : kblk;
-  s.smem = 1024 + size_t(s.stages) * stage + size_t(2 * (1 + sfb)) * kScaleBytes +
-           size_t(2 * s.stages + 5) * 8 + 16;
-  while (s.tcols < static_cast<uint32_t>(s.NB + 8 * (1 + sfb))) s.tcols <<= 1;
+  while (s.tcols < static_cast<uint32_t>(s.NB + 16)) s.tcols <<= 1;
   const int64_t work = int64_t(s.tiles) * s.ttiles;
   int64_t splits = 2 * int64_t(sm_count()) / work;
   if (splits > kSkMaxSplits) splits = kSkMaxSplits;
@@ -639,13 +701,20 @@ SkSched sk_sched(int64_t M, int64_t N, int64_t K) {
   const int gpcs = sm_count() / 18 > 1 ? sm_count() / 18 : 1;
   while (splits > 1 && (32 / splits) * gpcs < work) --splits;
   s.splits = static_cast<int>(splits < 1 ? 1 : splits);
+  // a ring as deep as the CTAs that share an SM allow, no deeper than the work
+  const size_t ring = size_t(work * s.splits > sm_count() ? 108 : 200) * 1024;
+  const int most = (kblk + s.splits - 1) / s.splits;
+  int st = static_cast<int>(ring / stage);
+  st = st < 2 ? 2 : (st > 8 ? 8 : st);
+  s.stages = st > most ? (most < 2 ? 2 : most) : st;
+  s.smem = 1024 + size_t(s.stages) * stage + size_t(4) * kScaleBytes +
+           size_t(2 * s.stages + 5) * 8 + 16;
   return s;
 }
 
 template <typename T>
 cudaError_t launch_rows(const uint8_t* xq, int64_t M, const uint8_t* wq, int64_t N, int64_t K,
-                        const LinQ8Params& p, cudaStream_t st) {
-  const SkSched s = sk_sched(M, N, K);
+                        const LinQ8Params& p, const SkSched& s, cudaStream_t st) {
   CUtensorMap tmW, tmX;
   if (!make_tmap_u8(&tmW, wq, N, K, K, kKB, 128) || !make_tmap_u8(&tmX, xq, M, K, K, kKB, s.NB))
     return cudaErrorInvalidValue;
@@ -660,6 +729,28 @@ cudaError_t launch_rows(const uint8_t* xq, int64_t M, const uint8_t* wq, int64_t
   return counted_launch(1);
 }
 
+// About how long the two kernels take, in us, fitted to both over M = 1 .. 4096
+// at the decoder's weights. Rows: the split sum grows with the width of x's
+// tile, a k-block of a CTA costs its MMAs and scales or its CTAs' share of HBM.
+// Pair: a start, then all of K for each wave of tiles. Measured rows / pair:
+// 1 x 9728 x 2560 8.6 / 25.2, 512 x 9728 x 2560 20.9 / 26.4, 1024 x 9728 x 2560
+// 37.8 / 28.2, 128 x 2560 x 6144 11.9 / 12.5, 256 x 2560 x 6144 14.0 / 11.9,
+// 64 x 2560 x 19456 15.3 / 17.5, 128 x 2560 x 19456 19.6 / 18.0,
+// 4 x 2560 x 151936 65 / 95.
+double rows_us(const SkSched& s, int kblk) {
+  const double ctas = double(s.tiles) * s.ttiles * s.splits, slots = 2.0 * sm_count();
+  const double waves = ctas > slots ? ctas / slots : 1.0, busy = ctas < slots ? ctas : slots;
+  const double mma = 0.15 + 0.0025 * s.NB, hbm = 0.0025 * busy;
+  return 5.5 + 0.035 * s.NB +
+         waves * ((kblk + s.splits - 1) / s.splits) * (mma > hbm ? mma : hbm);
+}
+double pair_us(int64_t M, int64_t N, int kblk) {
+  const int64_t tiles = ((M + 255) / 256) * ((N + 223) / 224), pairs = sm_count() / 2;
+  const int64_t waves = (tiles + pairs - 1) / pairs;
+  const double mma = 5.2 + 0.26 * double(waves) * (kblk + 4), hbm = 6 + 2e-5 * double(N) * kblk;
+  return mma > hbm ? mma : hbm;
+}
+
 }  // namespace
 
 cudaError_t launch_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
@@ -672,12 +763,18 @@ cudaError_t launch_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, co
   p.words = p.kblk % kSG == 0 && reinterpret_cast<uintptr_t>(xs) % 4 == 0 &&
             reinterpret_cast<uintptr_t>(ws) % 4 == 0;
   p.err = device_error_ptr();
-  const char* f8 = getenv("Q8F");
-  if (f8 ? f8[0] == 'r' : M <= 224)
-    return out_bf16 ? launch_rows<__nv_bfloat16>(xq, M, wq, N, K, p, st)
-                    : launch_rows<float>(xq, M, wq, N, K, p, st);
-  return out_bf16 ? launch_pair<__nv_bfloat16, 224>(xq, M, wq, N, K, p, st)
-                  : launch_pair<float, 224>(xq, M, wq, N, K, p, st);
+  const SkSched sk = sk_sched(M, N, K);
+  const bool rows = rows_us(sk, p.kblk) <= pair_us(M, N, p.kblk);
+  if (rows)
+    return out_bf16 ? launch_rows<__nv_bfloat16>(xq, M, wq, N, K, p, sk, st)
+                    : launch_rows<float>(xq, M, wq, N, K, p, sk, st);
+  const bool wide = N * (out_bf16 ? 2 : 4) % 32 == 0 && reinterpret_cast<uintptr_t>(out) % 32 == 0 &&
+                    reinterpret_cast<uintptr_t>(resid) % 32 == 0;
+  if (out_bf16)
+    return wide ? launch_pair<__nv_bfloat16, 224, true>(xq, M, wq, N, K, p, st)
+                : launch_pair<__nv_bfloat16, 224, false>(xq, M, wq, N, K, p, st);
+  return wide ? launch_pair<float, 224, true>(xq, M, wq, N, K, p, st)
+              : launch_pair<float, 224, false>(xq, M, wq, N, K, p, st);
 }
 
 }  // namespace q3vl
