@@ -1,103 +1,687 @@
-// Attention of one query row per sequence over the 8-bit cache (q8.cuh).
+// Attention of one query row per sequence over the 8-bit cache (q8.cuh):
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(q . k_t / sqrt(128) - max).
+//
+// Bound by the cache's bytes: 256 per token and KV head, read once for the
+// G = nh / nkv query heads that share it. The cache rows go from TMA to the
+// tensor core as they are stored, with no conversion: an e4m3 tile of 128
+// tokens is the MMA's M operand (kind::mxf8f6f4), once as K (tokens x dims)
+// and once as V transposed (dims x tokens). What multiplies them has to be e4m3 too,
+// so q and the probabilities are split into a sum of e4m3 parts, each 2^-4 of
+// the one before:
+//   q = 2^e (a1 + a2 / 16 + a3 / 256), exact for most bf16 values, and to
+//       2^-18 of the head's largest element for all;
+//   p = a1 + a2 / 16, to 2^-8 of p (the two halves of a step at 2^-4 each),
+//       or 2^-22 of the largest.
+// The parts are further columns of the narrow N operand, whose width costs
+// nothing: an MMA of 128 x N x 32 takes as long as its 4 KB of M operand do.
+// The factors 2^e, 2^-4i and the scale of the V block are E8M0 scales that the
+// tensor core applies; the scale of the K block goes into the softmax's.
+//
+//   S^T [128 tokens x 3G] = K [128 x 128] . Q^T       O^T [128 dims x 2G] = V^T . P^T
+//
+// The chunks (128 tokens of one sequence and KV head) of all sequences form
+// one list; each CTA takes an equal, contiguous range of it, so uneven lengths
+// balance. A range covers segments of one or more (sequence, head); a segment
+// that is a whole (sequence, head) is finished in place, another leaves (o, max,
+// sum) in the workspace, in one of its CTA's two slots, and a second kernel
+// joins them in order (and writes the rows of sequences without tokens).
+//
+// Roles per CTA (224 threads, two CTAs per SM): warps 0-3 softmax (thread = token,
+// then dimension), warp 4 TMA, warp 5 MMA, warp 6 builds the q parts. Chunks go in
+// batches of kBat: the S MMAs of batch j + 1 run while batch j is in the
+// softmax, and K tiles are loaded one batch ahead of V tiles.
 #include "q3vl_internal.h"
 #include "q8.cuh"
 
 namespace q3vl {
 namespace {
 
+constexpr int kAqThreads = 224;
+constexpr int kAqTiles = 6;               // ring of 16 KB tiles, K and V in turn
+constexpr int kAqTile = 128 * 128;
+constexpr int kAqMaxB = 256;
+constexpr int kAqRec = 130;               // floats of a head's partial: o[128], max, sum
+
+template <int G>
+struct AqCfg {
+  static constexpr int NS = G == 8 ? 32 : 16;      // S columns: 3 G parts
+  static constexpr int kBat = G == 8 ? 2 : 4;      // chunks per batch
+  static constexpr int kQ = NS * 128;              // q parts, e4m3
+  static constexpr int kP = 16 * 128;              // p parts of a chunk
+  // TMEM columns: S of two batches, O, scales of K (ones), q (two segments), V, p
+  static constexpr int cS = 0, cO = 2 * kBat * NS, cSfK = cO + 16, cSfQ = cSfK + 4,
+                       cSfV = cSfQ + 8, cSfP = cSfV + 4;
+  static constexpr uint32_t kCols = 256;
+  static_assert(cSfP + 4 <= 256, "TMEM columns");
+  static constexpr size_t kSmem = 1024 + size_t(kAqTiles) * kAqTile + size_t(kBat) * kP +
+                                  2 * kQ + 2 * 512 + (kAqMaxB + 1) * 4 + 2 * 4 * 8 * 4 + 4 * 8 * 4 +
+                                  (2 * kAqTiles + 9) * 8 + 64;
+  static_assert(kSmem <= 115712, "two CTAs per SM");
+};
+
 struct AttnQ8Params {
   const __nv_bfloat16* q;   // [B][nh*128]
-  const uint8_t* kc;        // the cache [n_seq][cap][nkv*128]
-  const uint8_t* vc;
   const uint8_t* ks;        // scales [n_seq][nblk][nkv]
   const uint8_t* vs;
   int64_t cap;
   int n_seq, nblk;
   const int32_t* seq;
   const int32_t* len;
-  int plus;
-  int B, nkv, G;
+  int plus;                 // tokens attended: len[b] + plus
+  int early;                // all blocks but each sequence's last are final before the dependency
+  int B, nkv;
+  int ctas;                 // of the main kernel
   float scale_log2;         // log2(e) / sqrt(128)
   __nv_bfloat16* o;         // [B][nh*128]
+  float* part;              // [ctas][2][G][kAqRec]
   int32_t* err;
 };
 
-// One block of 128 threads per (sequence, query head): thread t scores token
-// t of each 128-token block, then sums dimension t over the block's tokens.
-__global__ void __launch_bounds__(128) attn_q8_kernel(AttnQ8Params p) {
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int nh = p.G * p.nkv, b = blockIdx.x / nh, h = blockIdx.x % nh, g = h / p.G;
-  __shared__ float s_q[128], s_p[128], s_r[4];
-  griddep_wait();
-  const int slot = p.seq[b], L = p.len[b] + p.plus;
-  const bool ok = slot >= 0 && slot < p.n_seq && L >= p.plus && int64_t(L) <= p.cap;
-  if (!ok && t == 0) record_error(p.err, Q3VL_ERANGE, kWhereAttnQ8Range);
-  const int n = ok ? L : 0;
-  s_q[t] = __bfloat162float(p.q[(int64_t(b) * nh + h) * 128 + t]) * p.scale_log2;
-  __syncthreads();
-  const int64_t rs = int64_t(p.nkv) * 128;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int c = 0; c * 128 < n; ++c) {
-    const int64_t row0 = int64_t(slot) * p.cap + c * 128;
-    const int64_t si = (int64_t(slot) * p.nblk + c) * p.nkv + g;
-    float s = -INFINITY;
-    if (c * 128 + t < n) {
-      const uint32_t* kr = reinterpret_cast<const uint32_t*>(p.kc + (row0 + t) * rs + g * 128);
-      float d = 0.f;
-      for (int i = 0; i < 32; ++i) {
-        const float4 x = unpack_e4m3x4(kr[i]);
-        d += x.x * s_q[4 * i] + x.y * s_q[4 * i + 1] + x.z * s_q[4 * i + 2] + x.w * s_q[4 * i + 3];
-      }
-      s = d * e8m0_scale(p.ks[si]);
-    }
-    float w = warp_max(s);
-    if (lane == 0) s_r[warp] = w;
-    __syncthreads();
-    const float M = fmaxf(m, fmaxf(fmaxf(s_r[0], s_r[1]), fmaxf(s_r[2], s_r[3])));
-    const float e = s == -INFINITY ? 0.f : exp2f(s - M);
-    s_p[t] = e;
-    __syncthreads();
-    w = warp_sum(e);
-    if (lane == 0) s_r[warp] = w;
-    __syncthreads();
-    const float a = m == -INFINITY ? 0.f : exp2f(m - M);
-    l = l * a + (s_r[0] + s_r[1] + s_r[2] + s_r[3]);
-    float o = 0.f;
-    for (int i = 0; i < 128 && c * 128 + i < n; ++i) {
-      const uint32_t x = p.vc[(row0 + i) * rs + g * 128 + t];
-      o += s_p[i] * unpack_e4m3x4(x).x;
-    }
-    acc = acc * a + o * e8m0_scale(p.vs[si]);
-    m = M;
-    __syncthreads();
+// Chunks of sequence b's tokens (0: none, or out of range).
+__device__ __forceinline__ int aq_chunks(const AttnQ8Params& p, int b, bool& ok) {
+  const int slot = p.seq[b], L = p.len[b];
+  ok = slot >= 0 && slot < p.n_seq && L >= 0 && int64_t(L) + p.plus <= p.cap;
+  return ok ? (L + p.plus + 127) / 128 : 0;
+}
+
+// A batch: chunks c .. c + nb - 1 of KV head g of sequence b, inside a segment
+// [c0, c1) of the sequence's nc chunks.
+struct AqBatch {
+  int b, g, slot, len, nc, c0, c1, c, nb;
+  __device__ bool first() const { return c == c0; }
+  __device__ bool last() const { return c + nb == c1; }
+};
+
+// The batches of this CTA's range of the chunk list (pref: chunks before each
+// sequence, all its heads counted).
+template <int kBat>
+struct AqIter {
+  const AttnQ8Params& p;
+  const int* pref;
+  int64_t u, u1;
+  AqBatch t{};
+  __device__ AqIter(const AttnQ8Params& p_, const int* pref_) : p(p_), pref(pref_) {
+    const int64_t total = pref[p.B];
+    u = total * blockIdx.x / gridDim.x;
+    u1 = total * (blockIdx.x + 1) / gridDim.x;
   }
-  p.o[(int64_t(b) * nh + h) * 128 + t] = __float2bfloat16_rn(n > 0 ? acc / l : 0.f);
+  __device__ bool next(AqBatch& out) {
+    if (t.c + t.nb < t.c1) {
+      t.c += t.nb;
+    } else {
+      if (u >= u1) return false;
+      int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before u
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pref[mid] <= u) lo = mid;
+        else hi = mid - 1;
+      }
+      const int at = static_cast<int>(u - pref[lo]);
+      t.b = lo;
+      t.nc = (pref[lo + 1] - pref[lo]) / p.nkv;
+      t.g = at / t.nc;
+      t.c0 = at % t.nc;
+      const int64_t left = u1 - u;
+      t.c1 = left < t.nc - t.c0 ? t.c0 + static_cast<int>(left) : t.nc;
+      u += t.c1 - t.c0;
+      t.c = t.c0;
+      t.slot = p.seq[lo];
+      t.len = p.len[lo] + p.plus;
+    }
+    t.nb = min(kBat, t.c1 - t.c);
+    out = t;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t w) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
+
+template <int G>
+__global__ void __launch_bounds__(kAqThreads, 2)
+attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               AttnQ8Params p) {
+  using C = AqCfg<G>;
+  constexpr int NS = C::NS, kBat = C::kBat;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* s_tile = smem;                                  // [kAqTiles][128 x 128]
+  uint8_t* s_p = s_tile + kAqTiles * kAqTile;              // [kBat][16 x 128]
+  uint8_t* s_q = s_p + kBat * C::kP;                       // [2][NS x 128]
+  uint8_t* s_qs = s_q + 2 * C::kQ;                         // [2][512] scale words of the q parts
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_qs + 2 * 512);
+  uint64_t* empty = full + kAqTiles;
+  uint64_t* s_full = empty + kAqTiles;                     // [2]
+  uint64_t* q_full = s_full + 2;                           // [2]
+  uint64_t* q_empty = q_full + 2;                          // [2]
+  uint64_t* p_full = q_empty + 2;
+  uint64_t* o_full = p_full + 1;
+  uint64_t* drain = o_full + 1;
+  float* s_wm = reinterpret_cast<float*>(drain + 1);      // [2][4 warps][8] maxima
+  float* s_wl = s_wm + 2 * 4 * 8;                          // [4 warps][8] sums
+  int* s_pref = reinterpret_cast<int*>(s_wl + 4 * 8);      // [B + 1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pref + kAqMaxB + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (t == 0) {
+    for (int i = 0; i < kAqTiles; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1); mbar_init(q_full + i, 1); mbar_init(q_empty + i, 1);
+    }
+    mbar_init(p_full, 4);
+    mbar_init(o_full, 1);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+  griddep_launch_dependents();
+  if (!p.early) griddep_wait();
+  if (warp == 6) {
+    // chunks before each sequence: lane l owns sequences 8 l .. 8 l + 7
+    int n[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int b = 8 * lane + i;
+      bool ok = true;
+      n[i] = b < p.B ? p.nkv * aq_chunks(p, b, ok) : 0;
+      if (!ok && blockIdx.x == 0) record_error(p.err, Q3VL_ERANGE, kWhereAttnQ8Range);
+      sum += n[i];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    int at = inc - sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (8 * lane + i <= p.B) s_pref[8 * lane + i] = at;
+      at += n[i];
+    }
+    if (lane == 31 && p.B == kAqMaxB) s_pref[kAqMaxB] = at;
+  } else if (warp < 4) {
+    // p parts of the columns from 2 G on stay zero
+    for (int i = t; i < kBat * C::kP / 16; i += 128)
+      *reinterpret_cast<uint4*>(s_p + 16 * i) = make_uint4(0, 0, 0, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t lf = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  if (warp < 4) {
+    // constant scales: ones for K and for the first p parts, 2^-4 for the second
+    tmem_st4(tmem + lf + C::cSfK, kNoScale);
+    tmem_st4(tmem + lf + C::cSfP, lane < G ? kNoScale : 0x7b7b7b7bu);
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  if (warp == 4) {
+    AqIter<kBat> ik(p, s_pref), iv(p, s_pref);
+    AqBatch bk, bv;
+    int stage = 0, issued = 0;
+    uint32_t ph = 1;
+    bool ok = true, waited = !p.early;
+    auto load = [&](const AqBatch& a, const CUtensorMap* tm) {
+      for (int i = 0; i < a.nb && ok; ++i) {
+        if (!waited && a.c + i == a.nc - 1) {  // the block with the newest row
+          griddep_wait();
+          waited = true;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, ph, p.err, kWhereAttnQ8, s_abort));
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full + stage, kAqTile);
+          tma_load_2d(s_tile + stage * kAqTile, tm, full + stage, a.g * 128,
+                      static_cast<int32_t>(int64_t(a.slot) * p.cap + int64_t(a.c + i) * 128));
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == kAqTiles) { stage = 0; ph ^= 1; }
+      }
+    };
+    if (ik.next(bk)) load(bk, &tmK);
+    while (ok && iv.next(bv)) {
+      if (ik.next(bk)) load(bk, &tmK);
+      if (ok) load(bv, &tmV);
+    }
+    // every issued load lands before the CTA may exit
+    for (int i = issued > kAqTiles ? issued - kAqTiles : 0; i < issued; ++i)
+      mbar_wait(full + i % kAqTiles, (i / kAqTiles) & 1, p.err, kWhereAttnQ8, nullptr);
+    if (!waited) griddep_wait();
+  } else if (warp == 5) {
+    constexpr uint32_t id_s = idesc_mxf8(128, NS), id_o = idesc_mxf8(128, 16) | (1u << 15);
+    AqIter<kBat> is(p, s_pref), iv(p, s_pref);
+    AqBatch bs, bv;
+    int stage = 0, js = 0, jv = 0, seg = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    auto step = [&]() { if (++stage == kAqTiles) { stage = 0; ph ^= 1; } };
+    auto wait = [&](uint64_t* bar, uint32_t par) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, par, p.err, kWhereAttnQ8, s_abort));
+    };
+    auto scores = [&](const AqBatch& a) {
+      const int qb = seg & 1;
+      const uint32_t sfq = tmem + C::cSfQ + 4 * qb;
+      if (a.first()) {
+        ok = wait(q_full + qb, (seg >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t ds = sdesc_scales(smem_u32(s_qs + qb * 512));
+        if (elect_one()) tmem_cp_scales(sfq, ds);
+        __syncwarp();
+      }
+      const uint64_t dq = sdesc_sw128(smem_u32(s_q + qb * C::kQ), 16, 1024);
+      for (int i = 0; i < a.nb; ++i) {
+        ok = wait(full + stage, ph);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t dk = sdesc_sw128(smem_u32(s_tile + stage * kAqTile), 16, 1024);
+        const uint32_t d = tmem + C::cS + ((js & 1) * kBat + i) * NS;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_mxf8_ss(d, dk + 2 * kk, dq + 2 * kk, id_s, tmem + C::cSfK, sfq, kk > 0 ? 1u : 0u);
+          umma_commit(empty + stage);
+        }
+        __syncwarp();
+        step();
+      }
+      if (elect_one()) {
+        umma_commit(s_full + (js & 1));
+        if (a.last()) umma_commit(q_empty + qb);
+      }
+      __syncwarp();
+      ++js;
+      if (a.last()) ++seg;
+    };
+    if (is.next(bs)) scores(bs);
+    while (ok && iv.next(bv)) {
+      if (is.next(bs)) scores(bs);
+      if (!ok || !wait(p_full, jv & 1)) break;
+      tc_fence_after();
+      for (int i = 0; i < bv.nb; ++i) {
+        ok = wait(full + stage, ph);
+        if (!ok) break;
+        tc_fence_after();
+        uint8_t* v = s_tile + stage * kAqTile;
+        const int rows = bv.len - (bv.c + i) * 128;
+        if (rows < 128) {
+          // rows behind the sequence hold whatever the cache had: zero, for
+          // 0 * NaN would not be
+          for (int k = rows * 8 + lane; k < 128 * 8; k += 32)
+            *reinterpret_cast<uint4*>(v + 16 * k) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint64_t dv = sdesc_sw128(smem_u32(v), 16, 1024);
+        const uint64_t dp = sdesc_sw128(smem_u32(s_p + i * C::kP), 16, 1024);
+        const uint32_t id = id_o | (static_cast<uint32_t>(i) << 29);  // V's scale: byte i
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_mxf8_ss(tmem + C::cO, dv + 256 * kk, dp + 2 * kk, id, tmem + C::cSfV,
+                         tmem + C::cSfP, (i | kk) > 0 ? 1u : 0u);
+          umma_commit(empty + stage);
+          if (i == bv.nb - 1) umma_commit(o_full);
+        }
+        __syncwarp();
+        step();
+      }
+      ++jv;
+    }
+    if (!ok) *s_abort = 1;
+    // all issued MMAs complete before the TMEM is released
+    if (elect_one()) umma_commit(drain);
+    __syncwarp();
+    mbar_wait(drain, 0, p.err, kWhereAttnQ8, nullptr);
+  } else if (warp == 6) {
+    griddep_wait();
+    // q parts: row n = part * G + h of the N operand, and its scale
+    for (int i = lane; i < 2 * C::kQ / 16; i += 32)
+      *reinterpret_cast<uint4*>(s_q + 16 * i) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    AqIter<kBat> it(p, s_pref);
+    AqBatch a;
+    int seg = 0;
+    while (it.next(a)) {
+      if (!a.first()) continue;
+      const int qb = seg & 1;
+      if (seg >= 2 &&
+          !__all_sync(0xffffffffu, mbar_wait(q_empty + qb, ((seg >> 1) - 1) & 1, p.err,
+                                             kWhereAttnQ8, s_abort)))
+        break;
+      const __nv_bfloat16* src = p.q + (int64_t(a.b) * p.nkv + a.g) * G * 128 + 4 * lane;
+      uint2 raw[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) raw[h] = *reinterpret_cast<const uint2*>(src + h * 128);
+      uint32_t word = kNoScale;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float2 x = unpack_bf16x2(raw[h].x), y = unpack_bf16x2(raw[h].y);
+        float f[4] = {x.x, x.y, y.x, y.y};
+        const float am = redux_max(fmaxf(fmaxf(finite_abs(f[0]), finite_abs(f[1])),
+                                         fmaxf(finite_abs(f[2]), finite_abs(f[3]))));
+        const uint32_t e = max(e8m0_of_amax(am), 16u);  // room for the parts' smaller scales
+        const float inv = e8m0_inverse(e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] *= inv;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const int n = part * G + h;
+          const uint32_t w = pack_e4m3x4(f[0], f[1], f[2], f[3]);
+          const float4 r = unpack_e4m3x4(w);
+          f[0] = (f[0] - r.x) * 16.f; f[1] = (f[1] - r.y) * 16.f;
+          f[2] = (f[2] - r.z) * 16.f; f[3] = (f[3] - r.w) * 16.f;
+          *reinterpret_cast<uint32_t*>(s_q + qb * C::kQ + n * 128 +
+                                       (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = w;
+          if (lane == n) word = (e - 4 * part) * 0x01010101u;
+        }
+      }
+      *reinterpret_cast<uint4*>(s_qs + qb * 512 + lane * 16) =
+          make_uint4(word, kNoScale, kNoScale, kNoScale);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full + qb);
+      ++seg;
+    }
+  } else {
+    // A wait that gives up raises s_abort, which makes every later one return
+    // at once: these warps then walk through the rest without results, so that
+    // all four pass the same named barriers.
+    griddep_wait();
+    AqIter<kBat> it(p, s_pref);
+    AqBatch a;
+    int j = 0;
+    float m_run[G], l_run[G], o_run[G], fade[G];
+    while (it.next(a)) {
+      if (a.first()) {
+#pragma unroll
+        for (int h = 0; h < G; ++h) { m_run[h] = -INFINITY; l_run[h] = o_run[h] = fade[h] = 0.f; }
+      }
+      // scales of the batch's blocks, requested ahead of the scores
+      const int64_t si = (int64_t(a.slot) * p.nblk + a.c) * p.nkv + a.g;
+      uint8_t kb[kBat], vb[kBat];
+#pragma unroll
+      for (int i = 0; i < kBat; ++i) {
+        const int64_t at = si + int64_t(min(i, a.nb - 1)) * p.nkv;
+        kb[i] = p.ks[at];
+        vb[i] = p.vs[at];
+      }
+      mbar_wait(s_full + (j & 1), (j >> 1) & 1, p.err, kWhereAttnQ8, s_abort);
+      __syncwarp();
+      tc_fence_after();
+      float sc[kBat][G];
+#pragma unroll
+      for (int i = 0; i < kBat; ++i) {
+        uint32_t u[NS];
+        if (i < a.nb) {
+          const uint32_t at = tmem + lf + C::cS + ((j & 1) * kBat + i) * NS;
+          if constexpr (NS == 16) tmem_ld16(at, u);
+          else tmem_ld32(at, u);
+          tmem_ld_wait();
+        }
+        const bool sees = i < a.nb && (a.c + i) * 128 + t < a.len;
+        const float f = e8m0_scale(kb[i]) * p.scale_log2;
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+          sc[i][h] = sees ? ((__uint_as_float(u[h]) + __uint_as_float(u[G + h])) +
+                             __uint_as_float(u[2 * G + h])) * f
+                          : -INFINITY;
+      }
+      float* wm = s_wm + (j & 1) * 32;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        float v = sc[0][h];
+#pragma unroll
+        for (int i = 1; i < kBat; ++i) v = fmaxf(v, sc[i][h]);
+        v = redux_max(v);
+        if (lane == 0) wm[warp * 8 + h] = v;
+      }
+      softmax_sync();
+      float next_fade[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float M = fmaxf(fmaxf(fmaxf(wm[h], wm[8 + h]), fmaxf(wm[16 + h], wm[24 + h])),
+                              m_run[h]);
+        next_fade[h] = ex2_approx(m_run[h] - M);
+        m_run[h] = M;
+        float l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kBat; ++i) {
+          // 2^8 p: the sums carry the factor as well, and the quotient drops it
+          sc[i][h] = ex2_approx(sc[i][h] - M + 8.f);
+          l += sc[i][h];
+        }
+        l_run[h] = l_run[h] * next_fade[h] + l;
+      }
+      // the batch before: its products, behind which P and V's scales are free
+      auto fold = [&](int of) {
+        mbar_wait(o_full, of & 1, p.err, kWhereAttnQ8, s_abort);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t u[16];
+        tmem_ld16(tmem + lf + C::cO, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+          o_run[h] = o_run[h] * fade[h] + (__uint_as_float(u[h]) + __uint_as_float(u[G + h]));
+      };
+      if (!a.first()) fold(j - 1);
+#pragma unroll
+      for (int h = 0; h < G; ++h) fade[h] = next_fade[h];
+      uint32_t vw = 0;
+#pragma unroll
+      for (int i = 0; i < kBat; ++i) vw |= uint32_t(vb[i]) << (8 * i);
+      tmem_st4(tmem + lf + C::cSfV, vw);
+#pragma unroll
+      for (int i = 0; i < kBat; ++i) {
+        if (i >= a.nb) break;
+        uint8_t* dst = s_p + i * C::kP + (t & 15);
+        float v[(G + 3) / 4 * 4];
+#pragma unroll
+        for (int h = 0; h < (G + 3) / 4 * 4; ++h) v[h] = h < G ? sc[i][h < G ? h : 0] : 0.f;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int h0 = 0; h0 < G; h0 += 4) {
+            const uint32_t w = pack_e4m3x4(v[h0], v[h0 + 1], v[h0 + 2], v[h0 + 3]);
+            if (part == 0) {
+              const float4 r = unpack_e4m3x4(w);
+              v[h0] = (v[h0] - r.x) * 16.f; v[h0 + 1] = (v[h0 + 1] - r.y) * 16.f;
+              v[h0 + 2] = (v[h0 + 2] - r.z) * 16.f; v[h0 + 3] = (v[h0 + 3] - r.w) * 16.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (h0 + k < G) {
+                const int n = part * G + h0 + k;
+                dst[n * 128 + (((t >> 4) ^ (n & 7)) << 4)] = static_cast<uint8_t>(w >> (8 * k));
+              }
+          }
+      }
+      tmem_st_wait();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      if (a.last()) {
+        fold(j);
+        tc_fence_before();
+        // the sum over the threads' tokens
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float l = warp_sum(l_run[h]);
+          if (lane == 0) s_wl[warp * 8 + h] = l;
+        }
+        softmax_sync();
+        const bool whole = a.c0 == 0 && a.c1 == a.nc;
+        __nv_bfloat16* ob = p.o + (int64_t(a.b) * p.nkv + a.g) * G * 128 + t;
+        float* pb = p.part + (int64_t(blockIdx.x) * 2 + (a.c0 == 0 ? 1 : 0)) * G * kAqRec;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float l = (s_wl[h] + s_wl[8 + h]) + (s_wl[16 + h] + s_wl[24 + h]);
+          if (whole) {
+            ob[h * 128] = __float2bfloat16_rn(o_run[h] / l);
+          } else {
+            pb[h * kAqRec + t] = o_run[h];
+            if (t == 0) { pb[h * kAqRec + 128] = m_run[h]; pb[h * kAqRec + 129] = l; }
+          }
+        }
+        softmax_sync();  // s_wl is free
+      }
+      ++j;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// Joins the segments of the (sequence, head) pairs that more than one CTA
+// worked on, in the order of their chunks:
+//   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s,
+// and writes zeros where there are no tokens. One block per sequence and query head.
+__global__ void __launch_bounds__(128) attn_q8_join_kernel(AttnQ8Params p, int G) {
+  __shared__ int s_a[4], s_b[4];
+  const int t = threadIdx.x, nh = G * p.nkv, b = blockIdx.x / nh, qh = blockIdx.x % nh;
+  const int g = qh / G, h = qh % G;
+  griddep_launch_dependents();
+  griddep_wait();
+  // chunks before b, and of all
+  int before = 0, all = 0;
+  for (int i = t; i < p.B; i += 128) {
+    bool ok;
+    const int n = p.nkv * aq_chunks(p, i, ok);
+    all += n;
+    before += i < b ? n : 0;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if ((t & 31) == 0) { s_a[t >> 5] = before; s_b[t >> 5] = all; }
+  __syncthreads();
+  before = s_a[0] + s_a[1] + s_a[2] + s_a[3];
+  const int64_t total = int64_t(s_b[0]) + s_b[1] + s_b[2] + s_b[3];
+  bool ok;
+  const int nc = aq_chunks(p, b, ok);
+  __nv_bfloat16* out = p.o + int64_t(blockIdx.x) * 128 + t;
+  if (nc == 0) {
+    *out = __float2bfloat16_rn(0.f);
+    return;
+  }
+  // CTA i has chunks [i total / ctas, (i + 1) total / ctas)
+  const int64_t u0 = before + int64_t(g) * nc;
+  const int i0 = static_cast<int>(((u0 + 1) * p.ctas - 1) / total);
+  const int i1 = static_cast<int>(((u0 + nc) * p.ctas - 1) / total);
+  if (i0 == i1) return;  // finished in place
+  float M = -INFINITY, num = 0.f, den = 0.f;
+  constexpr int kU = 8;  // segments requested at a time
+  for (int i = i0; i <= i1; i += kU) {
+    float m[kU], l[kU], o[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      // a CTA whose range is empty (more CTAs than chunks) has no record
+      const int64_t c = i + k;
+      const bool has = c <= i1 && total * c / p.ctas < total * (c + 1) / p.ctas;
+      const float* r = p.part + ((has ? c : i0) * 2 + (c == i0 || !has ? 1 : 0)) * G * kAqRec +
+                       h * kAqRec;
+      m[k] = has ? __ldcg(r + 128) : -INFINITY;
+      l[k] = has ? __ldcg(r + 129) : 0.f;
+      o[k] = has ? __ldcg(r + t) : 0.f;
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kU; ++k) top = fmaxf(top, m[k]);
+    const float f = ex2_approx(M - top);
+    num *= M == -INFINITY ? 0.f : f;
+    den *= M == -INFINITY ? 0.f : f;
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      if (i + k > i1 || l[k] == 0.f) continue;
+      const float w = ex2_approx(m[k] - top);
+      num = fmaf(w, o[k], num);
+      den = fmaf(w, l[k], den);
+    }
+    M = top;
+  }
+  *out = __float2bfloat16_rn(num / den);
+}
+
+int aq_ctas(int nkv, int B, int64_t cap) {
+  const int64_t most = int64_t(B) * nkv * ((cap + 127) / 128);
+  return static_cast<int>(most < 2 * sm_count() ? most : 2 * sm_count());
+}
+
+template <int G>
+cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnQ8Params& p,
+                     cudaStream_t st) {
+  auto kern = attn_q8_kernel<G>;
+  cudaError_t e = smem_attr_at_least(reinterpret_cast<const void*>(kern), AqCfg<G>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_plain(kern, dim3(p.ctas), dim3(kAqThreads), AqCfg<G>::kSmem, st, tmK, tmV, p);
 }
 
 }  // namespace
 
 size_t attention_q8_ws_bytes(const q3vl_config& c, int B, int64_t cap) {
-  (void)c; (void)B; (void)cap;
-  return 256;
+  const int G = c.n_heads / c.n_kv_heads;
+  return align256(size_t(aq_ctas(c.n_kv_heads, B, cap)) * 2 * G * kAqRec * sizeof(float));
 }
 
 cudaError_t launch_attention_q8(const q3vl_config& c, const void* q, int B,
                                 const q3vl_kv_cache_q8& kv, const int32_t* seq,
                                 const int32_t* len, int plus, bool early, void* o, void* ws,
                                 cudaStream_t st) {
-  (void)early; (void)ws;
+  const uint64_t rows = uint64_t(kv.n_seq) * uint64_t(kv.cap), dkv = uint64_t(kv_dim(c));
+  CUtensorMap tmK, tmV;
+  if (!make_tmap_u8(&tmK, kv.k, rows, dkv, dkv, 128, 128) ||
+      !make_tmap_u8(&tmV, kv.v, rows, dkv, dkv, 128, 128))
+    return cudaErrorInvalidValue;
   AttnQ8Params p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
-  p.kc = kv.k; p.vc = kv.v; p.ks = kv.k_scale; p.vs = kv.v_scale;
+  p.ks = kv.k_scale; p.vs = kv.v_scale;
   p.cap = kv.cap; p.n_seq = kv.n_seq; p.nblk = static_cast<int>((kv.cap + 127) / 128);
-  p.seq = seq; p.len = len; p.plus = plus;
-  p.B = B; p.nkv = c.n_kv_heads; p.G = c.n_heads / c.n_kv_heads;
+  p.seq = seq; p.len = len; p.plus = plus; p.early = early ? 1 : 0;
+  p.B = B; p.nkv = c.n_kv_heads;
+  p.ctas = aq_ctas(c.n_kv_heads, B, kv.cap);
   p.scale_log2 = static_cast<float>(1.4426950408889634 / 11.313708498984761);
   p.o = static_cast<__nv_bfloat16*>(o);
+  p.part = static_cast<float*>(ws);
   p.err = device_error_ptr();
-  const cudaError_t e = launch_pdl_plain(attn_q8_kernel, dim3(B * c.n_heads), dim3(128), 0, st, p);
+  const int G = c.n_heads / c.n_kv_heads;
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (G) {
+    case 1: e = launch_g<1>(tmK, tmV, p, st); break;
+    case 2: e = launch_g<2>(tmK, tmV, p, st); break;
+    case 4: e = launch_g<4>(tmK, tmV, p, st); break;
+    case 8: e = launch_g<8>(tmK, tmV, p, st); break;
+    default: break;
+  }
   if (e != cudaSuccess) return e;
-  return counted_launch(1);
+  e = launch_pdl_plain(attn_q8_join_kernel, dim3(B * c.n_heads), dim3(128), 0, st, p, G);
+  if (e != cudaSuccess) return e;
+  return counted_launch(2);
 }
 
 }  // namespace q3vl

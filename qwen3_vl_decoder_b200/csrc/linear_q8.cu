@@ -133,7 +133,6 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int k, int en
   for (int i = 0; i < kSG; ++i) w |= uint32_t(__ldg(row + min(k + i, end - 1))) << (8 * i);
   return w;
 }
-constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // 2^0
 
 // ---------------------------------------------------------------------------
 // Few rows: the weight is the MMA's M operand (128 rows a tile) and a tile of

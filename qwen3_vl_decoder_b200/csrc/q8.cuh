@@ -133,6 +133,7 @@ __device__ __forceinline__ void umma_mxf8_ss_pair(uint32_t d_tmem, uint64_t a_de
 // r at (r % 32) * 16 + (r / 32) * 4, copied to 4 TMEM columns (row r in lane
 // r % 32 of column r / 32, in all four 32-lane quarters). A copy and the MMAs
 // that one thread issues behind it run in that order.
+constexpr uint32_t kNoScale = 0x7f7f7f7fu;  // 2^0
 __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
   // no swizzle; 8-row groups of 128 bytes, one 16-byte column
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
