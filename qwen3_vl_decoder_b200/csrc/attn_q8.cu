@@ -19,12 +19,14 @@
 //
 //   S^T [128 tokens x 3G] = K [128 x 128] . Q^T       O^T [128 dims x 2G] = V^T . P^T
 //
-// The chunks (128 tokens of one sequence and KV head) of all sequences form
-// one list; each CTA takes an equal, contiguous range of it, so uneven lengths
-// balance. A range covers segments of one or more (sequence, head); a segment
-// that is a whole (sequence, head) is finished in place, another leaves (o, max,
-// sum) in the workspace, in one of its CTA's two slots, and a second kernel
-// joins them in order (and writes the rows of sequences without tokens).
+// The chunks (128 tokens) of all sequences form one list, cut into equal,
+// contiguous parts, so that uneven lengths balance; a part is worked on by nkv
+// neighbouring CTAs, one per KV head, which read the same rows of the cache at
+// about the same time (with the heads one after the other in the list, XXX).
+// A part covers segments of one or more sequences; a segment that is a whole
+// sequence is finished in place, another leaves (o, max, sum) in the
+// workspace, in one of its CTA's two slots, and a second kernel joins them in
+// order (and writes the rows of sequences without tokens).
 //
 // Roles per CTA (224 threads, two CTAs per SM): warps 0-3 softmax (thread = token,
 // then dimension), warp 4 TMA, warp 5 MMA, warp 6 builds the q parts. Chunks go in
@@ -70,10 +72,10 @@ struct AttnQ8Params {
   int plus;                 // tokens attended: len[b] + plus
   int early;                // all blocks but each sequence's last are final before the dependency
   int B, nkv;
-  int ctas;                 // of the main kernel
+  int parts;                // of the chunk list; nkv CTAs each
   float scale_log2;         // log2(e) / sqrt(128)
   __nv_bfloat16* o;         // [B][nh*128]
-  float* part;              // [ctas][2][G][kAqRec]
+  float* part;              // [parts][nkv][2][G][kAqRec]
   int32_t* err;
 };
 
@@ -92,18 +94,28 @@ struct AqBatch {
   __device__ bool last() const { return c + nb == c1; }
 };
 
-// The batches of this CTA's range of the chunk list (pref: chunks before each
-// sequence, all its heads counted).
+// Part i of `parts` has chunks [i total / parts, (i + 1) total / parts) of the
+// list; there are no more parts than chunks. At most 256 sequences of 1024
+// chunks and some hundred parts: the products stay in 32 bits.
+__device__ __forceinline__ int aq_parts_of(const AttnQ8Params& p, int total) {
+  return min(p.parts, total);
+}
+
+// The batches of this CTA's part of the chunk list (pref: chunks before each
+// sequence).
 template <int kBat>
 struct AqIter {
   const AttnQ8Params& p;
   const int* pref;
-  int64_t u, u1;
+  int u = 0, u1 = 0;
   AqBatch t{};
   __device__ AqIter(const AttnQ8Params& p_, const int* pref_) : p(p_), pref(pref_) {
-    const int64_t total = pref[p.B];
-    u = total * blockIdx.x / gridDim.x;
-    u1 = total * (blockIdx.x + 1) / gridDim.x;
+    const int total = pref[p.B], part = blockIdx.x / p.nkv, parts = aq_parts_of(p, total);
+    if (part < parts) {
+      u = static_cast<int>(static_cast<uint32_t>(total * part) / static_cast<uint32_t>(parts));
+      u1 = static_cast<int>(static_cast<uint32_t>(total * (part + 1)) / static_cast<uint32_t>(parts));
+    }
+    t.g = static_cast<int>(blockIdx.x % p.nkv);
   }
   __device__ bool next(AqBatch& out) {
     if (t.c + t.nb < t.c1) {
@@ -116,13 +128,10 @@ struct AqIter {
         if (pref[mid] <= u) lo = mid;
         else hi = mid - 1;
       }
-      const int at = static_cast<int>(u - pref[lo]);
       t.b = lo;
-      t.nc = (pref[lo + 1] - pref[lo]) / p.nkv;
-      t.g = at / t.nc;
-      t.c0 = at % t.nc;
-      const int64_t left = u1 - u;
-      t.c1 = left < t.nc - t.c0 ? t.c0 + static_cast<int>(left) : t.nc;
+      t.nc = pref[lo + 1] - pref[lo];
+      t.c0 = u - pref[lo];
+      t.c1 = min(t.c0 + u1 - u, t.nc);
       u += t.c1 - t.c0;
       t.c = t.c0;
       t.slot = p.seq[lo];
@@ -198,7 +207,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     for (int i = 0; i < 8; ++i) {
       const int b = 8 * lane + i;
       bool ok = true;
-      n[i] = b < p.B ? p.nkv * aq_chunks(p, b, ok) : 0;
+      n[i] = b < p.B ? aq_chunks(p, b, ok) : 0;
       if (!ok && blockIdx.x == 0) record_error(p.err, Q3VL_ERANGE, kWhereAttnQ8Range);
       sum += n[i];
     }
@@ -559,78 +568,100 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   }
 }
 
-// Joins the segments of the (sequence, head) pairs that more than one CTA
-// worked on, in the order of their chunks:
+// Joins the segments of the sequences that more than one part holds, in the
+// order of their chunks:
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s,
-// and writes zeros where there are no tokens. One block per sequence and query head.
+// and writes zeros where there are no tokens. One block per sequence and query
+// head; the weights of all segments are made at once, thread = segment, then
+// thread = dimension.
+constexpr int kAqMaxParts = 512;
+
 __global__ void __launch_bounds__(128) attn_q8_join_kernel(AttnQ8Params p, int G) {
-  __shared__ int s_a[4], s_b[4];
+  __shared__ int s_i[8];
+  __shared__ float s_f[4];
+  __shared__ float s_w[kAqMaxParts];
   const int t = threadIdx.x, nh = G * p.nkv, b = blockIdx.x / nh, qh = blockIdx.x % nh;
-  const int g = qh / G, h = qh % G;
+  const int g = qh / G, h = qh % G, warp = t >> 5, lane = t & 31;
   griddep_launch_dependents();
-  griddep_wait();
+  if (!p.early) griddep_wait();
   // chunks before b, and of all
-  int before = 0, all = 0;
+  int before = 0, total = 0;
+  bool ok;
   for (int i = t; i < p.B; i += 128) {
-    bool ok;
-    const int n = p.nkv * aq_chunks(p, i, ok);
-    all += n;
+    const int n = aq_chunks(p, i, ok);
+    total += n;
     before += i < b ? n : 0;
   }
-  before = __reduce_add_sync(0xffffffffu, before);
-  all = __reduce_add_sync(0xffffffffu, all);
-  if ((t & 31) == 0) { s_a[t >> 5] = before; s_b[t >> 5] = all; }
-  __syncthreads();
-  before = s_a[0] + s_a[1] + s_a[2] + s_a[3];
-  const int64_t total = int64_t(s_b[0]) + s_b[1] + s_b[2] + s_b[3];
-  bool ok;
   const int nc = aq_chunks(p, b, ok);
-  __nv_bfloat16* out = p.o + int64_t(blockIdx.x) * 128 + t;
-  if (nc == 0) {
-    *out = __float2bfloat16_rn(0.f);
-    return;
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) { s_i[warp] = before; s_i[4 + warp] = total; }
+  __syncthreads();
+  before = s_i[0] + s_i[1] + s_i[2] + s_i[3];
+  total = s_i[4] + s_i[5] + s_i[6] + s_i[7];
+  const int parts = aq_parts_of(p, total);
+  int i0 = 0, n = 0;  // parts i0 .. i0 + n - 1
+  if (nc > 0) {
+    i0 = static_cast<int>(static_cast<uint32_t>((before + 1) * parts - 1) / static_cast<uint32_t>(total));
+    n = static_cast<int>(static_cast<uint32_t>((before + nc) * parts - 1) /
+                         static_cast<uint32_t>(total)) - i0 + 1;
   }
-  // CTA i has chunks [i total / ctas, (i + 1) total / ctas)
-  const int64_t u0 = before + int64_t(g) * nc;
-  const int i0 = static_cast<int>(((u0 + 1) * p.ctas - 1) / total);
-  const int i1 = static_cast<int>(((u0 + nc) * p.ctas - 1) / total);
-  if (i0 == i1) return;  // finished in place
-  float M = -INFINITY, num = 0.f, den = 0.f;
-  constexpr int kU = 8;  // segments requested at a time
-  for (int i = i0; i <= i1; i += kU) {
-    float m[kU], l[kU], o[kU];
+  if (p.early) griddep_wait();
+  __nv_bfloat16* out = p.o + int64_t(blockIdx.x) * 128 + t;
+  if (nc == 0) *out = __float2bfloat16_rn(0.f);
+  if (n <= 1) return;  // finished in place
+  // part i's record: its second slot where the sequence starts in it
+  auto rec = [&](int s) {
+    return p.part + ((int64_t(i0 + s) * p.nkv + g) * 2 + (s == 0 ? 1 : 0)) * G * kAqRec + h * kAqRec;
+  };
+  constexpr int kU = 16;  // segments requested at a time
+  float o[kU];
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      // a CTA whose range is empty (more CTAs than chunks) has no record
-      const int64_t c = i + k;
-      const bool has = c <= i1 && total * c / p.ctas < total * (c + 1) / p.ctas;
-      const float* r = p.part + ((has ? c : i0) * 2 + (c == i0 || !has ? 1 : 0)) * G * kAqRec +
-                       h * kAqRec;
-      m[k] = has ? __ldcg(r + 128) : -INFINITY;
-      l[k] = has ? __ldcg(r + 129) : 0.f;
-      o[k] = has ? __ldcg(r + t) : 0.f;
+  for (int k = 0; k < kU; ++k) o[k] = k < n ? __ldcg(rec(k) + t) : 0.f;
+  float m[kAqMaxParts / 128], l[kAqMaxParts / 128], M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kAqMaxParts / 128; ++k) {
+    const int s = t + 128 * k;
+    m[k] = s < n ? __ldcg(rec(s) + 128) : -INFINITY;
+    l[k] = s < n ? __ldcg(rec(s) + 129) : 0.f;
+    M = fmaxf(M, m[k]);
+  }
+  M = warp_max(M);
+  if (lane == 0) s_f[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(s_f[0], s_f[1]), fmaxf(s_f[2], s_f[3]));
+  __syncthreads();
+  float den = 0.f;
+#pragma unroll
+  for (int k = 0; k < kAqMaxParts / 128; ++k) {
+    const int s = t + 128 * k;
+    const float w = s < n ? ex2_approx(m[k] - M) : 0.f;
+    s_w[s] = w;
+    if (s < n) den = fmaf(w, l[k], den);
+  }
+  den = warp_sum(den);
+  if (lane == 0) s_f[warp] = den;
+  __syncthreads();
+  den = (s_f[0] + s_f[1]) + (s_f[2] + s_f[3]);
+  float num = 0.f;
+  for (int s = 0; s < n; s += kU) {
+    if (s > 0) {
+#pragma unroll
+      for (int k = 0; k < kU; ++k) o[k] = s + k < n ? __ldcg(rec(s + k) + t) : 0.f;
     }
-    float top = M;
 #pragma unroll
-    for (int k = 0; k < kU; ++k) top = fmaxf(top, m[k]);
-    const float f = ex2_approx(M - top);
-    num *= M == -INFINITY ? 0.f : f;
-    den *= M == -INFINITY ? 0.f : f;
-#pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      if (i + k > i1 || l[k] == 0.f) continue;
-      const float w = ex2_approx(m[k] - top);
-      num = fmaf(w, o[k], num);
-      den = fmaf(w, l[k], den);
-    }
-    M = top;
+    for (int k = 0; k < kU; ++k)
+      if (s + k < n) num = fmaf(s_w[s + k], o[k], num);
   }
   *out = __float2bfloat16_rn(num / den);
 }
 
-int aq_ctas(int nkv, int B, int64_t cap) {
-  const int64_t most = int64_t(B) * nkv * ((cap + 127) / 128);
-  return static_cast<int>(most < 2 * sm_count() ? most : 2 * sm_count());
+// Two CTAs per SM, and no more parts than there can be chunks.
+int aq_parts(int nkv, int B, int64_t cap) {
+  const int64_t most = int64_t(B) * ((cap + 127) / 128);
+  int64_t parts = 2 * sm_count() / nkv > 1 ? 2 * sm_count() / nkv : 1;
+  if (parts > kAqMaxParts) parts = kAqMaxParts;
+  return static_cast<int>(most < parts ? most : parts);
 }
 
 template <int G>
@@ -639,14 +670,14 @@ cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnQ
   auto kern = attn_q8_kernel<G>;
   cudaError_t e = smem_attr_at_least(reinterpret_cast<const void*>(kern), AqCfg<G>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_plain(kern, dim3(p.ctas), dim3(kAqThreads), AqCfg<G>::kSmem, st, tmK, tmV, p);
+  return launch_pdl_plain(kern, dim3(p.parts * p.nkv), dim3(kAqThreads), AqCfg<G>::kSmem, st, tmK, tmV, p);
 }
 
 }  // namespace
 
 size_t attention_q8_ws_bytes(const q3vl_config& c, int B, int64_t cap) {
   const int G = c.n_heads / c.n_kv_heads;
-  return align256(size_t(aq_ctas(c.n_kv_heads, B, cap)) * 2 * G * kAqRec * sizeof(float));
+  return align256(size_t(aq_parts(c.n_kv_heads, B, cap)) * c.n_kv_heads * 2 * G * kAqRec * sizeof(float));
 }
 
 cudaError_t launch_attention_q8(const q3vl_config& c, const void* q, int B,
@@ -664,7 +695,7 @@ cudaError_t launch_attention_q8(const q3vl_config& c, const void* q, int B,
   p.cap = kv.cap; p.n_seq = kv.n_seq; p.nblk = static_cast<int>((kv.cap + 127) / 128);
   p.seq = seq; p.len = len; p.plus = plus; p.early = early ? 1 : 0;
   p.B = B; p.nkv = c.n_kv_heads;
-  p.ctas = aq_ctas(c.n_kv_heads, B, kv.cap);
+  p.parts = aq_parts(c.n_kv_heads, B, kv.cap);
   p.scale_log2 = static_cast<float>(1.4426950408889634 / 11.313708498984761);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.part = static_cast<float*>(ws);
