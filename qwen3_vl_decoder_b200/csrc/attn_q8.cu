@@ -41,22 +41,21 @@ namespace {
 constexpr int kAqThreads = 224;
 constexpr int kAqTiles = 6;               // ring of 16 KB tiles, K and V in turn
 constexpr int kAqTile = 128 * 128;
-constexpr int kAqMaxB = 256;
 constexpr int kAqRec = 130;               // floats of a head's partial: o[128], max, sum
 
 template <int G>
 struct AqCfg {
   static constexpr int NS = G == 8 ? 32 : 16;      // S columns: 3 G parts
-  static constexpr int kBat = G == 8 ? 2 : 4;      // chunks per batch
+  static constexpr int kBat = 2;                   // chunks per batch
   static constexpr int kQ = NS * 128;              // q parts, e4m3
   static constexpr int kP = 16 * 128;              // p parts of a chunk
   // TMEM columns: S of two batches, O, scales of K (ones), q (two segments), V, p
   static constexpr int cS = 0, cO = 2 * kBat * NS, cSfK = cO + 16, cSfQ = cSfK + 4,
                        cSfV = cSfQ + 8, cSfP = cSfV + 4;
-  static constexpr uint32_t kCols = 256;
-  static_assert(cSfP + 4 <= 256, "TMEM columns");
+  static constexpr uint32_t kCols = G == 8 ? 256 : 128;
+  static_assert(cSfP + 4 <= kCols, "TMEM columns");
   static constexpr size_t kSmem = 1024 + size_t(kAqTiles) * kAqTile + size_t(kBat) * kP +
-                                  2 * kQ + 2 * 512 + (kAqMaxB + 1) * 4 + 2 * 4 * 8 * 4 + 4 * 8 * 4 +
+                                  2 * kQ + 2 * 512 + 2 * 4 * 8 * 4 + 4 * 8 * 4 +
                                   (2 * kAqTiles + 9) * 8 + 64;
   static_assert(kSmem <= 115712, "two CTAs per SM");
 };
@@ -101,19 +100,62 @@ __device__ __forceinline__ int aq_parts_of(const AttnQ8Params& p, int total) {
   return min(p.parts, total);
 }
 
-// The batches of this CTA's part of the chunk list (pref: chunks before each
-// sequence).
+// Chunks of the sequences of one lane, 8 l .. 8 l + 7, and how many come before
+// them. Every role's warp makes its own: no barrier stands between the lengths
+// and the first load.
+struct AqList {
+  uint32_t n[4];            // two counts (<= 1024) to a word
+  int base, total;
+  __device__ AqList(const AttnQ8Params& p, int lane, bool report) {
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int b = 8 * lane + i;
+      bool ok = true;
+      const int k = b < p.B ? aq_chunks(p, b, ok) : 0;
+      if (!ok && report) record_error(p.err, Q3VL_ERANGE, kWhereAttnQ8Range);
+      sum += k;
+      n[i / 2] = i & 1 ? n[i / 2] | (uint32_t(k) << 16) : uint32_t(k);
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    base = inc - sum;
+    total = __shfl_sync(0xffffffffu, inc, 31);
+  }
+  // The sequence that chunk u of the list belongs to (whole warp).
+  __device__ void find(int u, int& b, int& start, int& nc) const {
+    int at = base, hit = -1, k = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = (n[i / 2] >> (16 * (i & 1))) & 0xffff;
+      if (u >= at && u < at + c) { hit = i; start = at; k = c; }
+      at += c;
+    }
+    const int lane = threadIdx.x & 31;
+    const int src = __ffs(__ballot_sync(0xffffffffu, hit >= 0)) - 1;
+    b = __shfl_sync(0xffffffffu, 8 * lane + hit, src);
+    start = __shfl_sync(0xffffffffu, start, src);
+    nc = __shfl_sync(0xffffffffu, k, src);
+  }
+};
+
+// The batches of this CTA's part of the chunk list (whole warps).
 template <int kBat>
 struct AqIter {
   const AttnQ8Params& p;
-  const int* pref;
+  const AqList& list;
   int u = 0, u1 = 0;
   AqBatch t{};
-  __device__ AqIter(const AttnQ8Params& p_, const int* pref_) : p(p_), pref(pref_) {
-    const int total = pref[p.B], part = blockIdx.x / p.nkv, parts = aq_parts_of(p, total);
+  __device__ AqIter(const AttnQ8Params& p_, const AqList& l) : p(p_), list(l) {
+    const int part = blockIdx.x / p.nkv, parts = aq_parts_of(p, l.total);
     if (part < parts) {
-      u = static_cast<int>(static_cast<uint32_t>(total * part) / static_cast<uint32_t>(parts));
-      u1 = static_cast<int>(static_cast<uint32_t>(total * (part + 1)) / static_cast<uint32_t>(parts));
+      u = static_cast<int>(static_cast<uint32_t>(l.total * part) / static_cast<uint32_t>(parts));
+      u1 = static_cast<int>(static_cast<uint32_t>(l.total * (part + 1)) /
+                            static_cast<uint32_t>(parts));
     }
     t.g = static_cast<int>(blockIdx.x % p.nkv);
   }
@@ -122,20 +164,14 @@ struct AqIter {
       t.c += t.nb;
     } else {
       if (u >= u1) return false;
-      int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before u
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pref[mid] <= u) lo = mid;
-        else hi = mid - 1;
-      }
-      t.b = lo;
-      t.nc = pref[lo + 1] - pref[lo];
-      t.c0 = u - pref[lo];
+      int start = 0;
+      list.find(u, t.b, start, t.nc);
+      t.c0 = u - start;
       t.c1 = min(t.c0 + u1 - u, t.nc);
       u += t.c1 - t.c0;
       t.c = t.c0;
-      t.slot = p.seq[lo];
-      t.len = p.len[lo] + p.plus;
+      t.slot = p.seq[t.b];
+      t.len = p.len[t.b] + p.plus;
     }
     t.nb = min(kBat, t.c1 - t.c);
     out = t;
@@ -176,8 +212,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   uint64_t* drain = o_full + 1;
   float* s_wm = reinterpret_cast<float*>(drain + 1);      // [2][4 warps][8] maxima
   float* s_wl = s_wm + 2 * 4 * 8;                          // [4 warps][8] sums
-  int* s_pref = reinterpret_cast<int*>(s_wl + 4 * 8);      // [B + 1]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_pref + kAqMaxB + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_wl + 4 * 8);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -199,35 +234,13 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tmem_relinquish();
   }
   griddep_launch_dependents();
-  if (!p.early) griddep_wait();
-  if (warp == 6) {
-    // chunks before each sequence: lane l owns sequences 8 l .. 8 l + 7
-    int n[8], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int b = 8 * lane + i;
-      bool ok = true;
-      n[i] = b < p.B ? aq_chunks(p, b, ok) : 0;
-      if (!ok && blockIdx.x == 0) record_error(p.err, Q3VL_ERANGE, kWhereAttnQ8Range);
-      sum += n[i];
-    }
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    int at = inc - sum;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (8 * lane + i <= p.B) s_pref[8 * lane + i] = at;
-      at += n[i];
-    }
-    if (lane == 31 && p.B == kAqMaxB) s_pref[kAqMaxB] = at;
-  } else if (warp < 4) {
+  if (warp < 4) {
     // p parts of the columns from 2 G on stay zero
     for (int i = t; i < kBat * C::kP / 16; i += 128)
       *reinterpret_cast<uint4*>(s_p + 16 * i) = make_uint4(0, 0, 0, 0);
+  } else if (warp == 6) {
+    for (int i = lane; i < 2 * C::kQ / 16; i += 32)
+      *reinterpret_cast<uint4*>(s_q + 16 * i) = make_uint4(0, 0, 0, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -244,8 +257,11 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
 
+  // lengths and slots are inputs of the call, not of the kernel before
+  if (!p.early || warp < 4 || warp == 6) griddep_wait();
+  const AqList list(p, lane, blockIdx.x == 0 && warp == 4);
   if (warp == 4) {
-    AqIter<kBat> ik(p, s_pref), iv(p, s_pref);
+    AqIter<kBat> ik(p, list), iv(p, list);
     AqBatch bk, bv;
     int stage = 0, issued = 0;
     uint32_t ph = 1;
@@ -279,7 +295,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     if (!waited) griddep_wait();
   } else if (warp == 5) {
     constexpr uint32_t id_s = idesc_mxf8(128, NS), id_o = idesc_mxf8(128, 16) | (1u << 15);
-    AqIter<kBat> is(p, s_pref), iv(p, s_pref);
+    AqIter<kBat> is(p, list), iv(p, list);
     AqBatch bs, bv;
     int stage = 0, js = 0, jv = 0, seg = 0;
     uint32_t ph = 0;
@@ -364,12 +380,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     __syncwarp();
     mbar_wait(drain, 0, p.err, kWhereAttnQ8, nullptr);
   } else if (warp == 6) {
-    griddep_wait();
     // q parts: row n = part * G + h of the N operand, and its scale
-    for (int i = lane; i < 2 * C::kQ / 16; i += 32)
-      *reinterpret_cast<uint4*>(s_q + 16 * i) = make_uint4(0, 0, 0, 0);
-    __syncwarp();
-    AqIter<kBat> it(p, s_pref);
+    AqIter<kBat> it(p, list);
     AqBatch a;
     int seg = 0;
     while (it.next(a)) {
@@ -417,8 +429,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // A wait that gives up raises s_abort, which makes every later one return
     // at once: these warps then walk through the rest without results, so that
     // all four pass the same named barriers.
-    griddep_wait();
-    AqIter<kBat> it(p, s_pref);
+    AqIter<kBat> it(p, list);
     AqBatch a;
     int j = 0;
     float m_run[G], l_run[G], o_run[G], fade[G];
