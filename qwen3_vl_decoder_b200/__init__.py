@@ -56,8 +56,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the current device's current stream, without building a Stream object (3 us a call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
 
 
 def config(hidden, n_heads, n_kv_heads, intermediate, dtype="bf16", qkv_bias=False,
@@ -415,10 +417,23 @@ def _arg(t: torch.Tensor, name: str, dtypes, shape=None, device=None) -> None:
         raise Q3VLError(_abi.EINVAL, f"{name} must be contiguous")
 
 
+def _is(t, dtype, shape, index: int) -> bool:
+    """Whether _arg would accept t on CUDA device `index`, at a fraction of its cost."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.get_device() == index and t.is_contiguous())
+
+
+def _run(t: torch.Tensor, stream, call, *args):
+    """call(*args, stream handle) with t's device current (the library works on the current one)
+    and, where a stream is given, with it current, so that what `call` allocates belongs to it."""
+    if stream is None and t.is_cuda and t.get_device() == torch._C._cuda_getDevice():
+        return call(*args, torch._C._cuda_getCurrentRawStream(t.get_device()))
+    with _on(t, stream) as st:
+        return call(*args, st)
+
+
 class _on:
-    """Makes a tensor's device current for a call (the library works on the current one), and
-    the caller's stream if one is given, so that what the call allocates belongs to that stream;
-    gives the stream to launch on."""
+    """The device and stream guards of _run; gives the stream to launch on."""
 
     def __init__(self, t: torch.Tensor, stream=None):
         if t.device.type != "cuda":
@@ -465,13 +480,15 @@ def quantize_weight_q8(w: torch.Tensor, stream=None) -> LinearQ8:
         raise Q3VLError(_abi.EINVAL, f"w must be [N, K], not {tuple(w.shape)}")
     N, K = w.shape
     cfg = config(128, 1, 1, 128, "bf16" if w.dtype == torch.bfloat16 else "fp32")
-    with _on(w, stream) as st:
+
+    def call(st):
         wq = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=w.device)
         ws = torch.empty((-(-N // Q8_BLOCK), -(-K // Q8_BLOCK)), dtype=torch.float8_e8m0fnu,
                          device=w.device)
         _check(lib().q3vl_quantize_weight_q8(ctypes.byref(cfg), _ptr(w), N, K, _ptr(wq), _ptr(ws),
                                              st))
-    return LinearQ8(wq, ws)
+        return LinearQ8(wq, ws)
+    return _run(w, stream, call)
 
 
 def add_rms_norm_q8(cfg: Config, x: torch.Tensor, gain: Optional[torch.Tensor],
@@ -483,28 +500,34 @@ def add_rms_norm_q8(cfg: Config, x: torch.Tensor, gain: Optional[torch.Tensor],
     gain None quantises h without a norm. h: where to write the sum (x for in place); a new
     tensor by default.
     """
-    dt = (torch_dtype(cfg),)
-    _arg(x, "x", dt)
+    dt = torch_dtype(cfg)
+    _arg(x, "x", (dt,))
     if x.dim() != 2 or x.shape[1] != cfg.hidden:
         raise Q3VLError(_abi.EINVAL, f"x must be [S, {cfg.hidden}], not {tuple(x.shape)}")
-    S, H = x.shape
-    if gain is not None:
-        _arg(gain, "gain", dt, (H,), x.device)
+    shape, index = x.shape, x.get_device()
+    if gain is not None and not _is(gain, dt, shape[1:], index):
+        _arg(gain, "gain", (dt,), shape[1:], x.device)
     if delta is None:
         if h is not None and h is not x:
             raise Q3VLError(_abi.EINVAL, "without a delta, h is x")
         h = x
     else:
-        _arg(delta, "delta", dt, (S, H), x.device)
-        if h is not None:
-            _arg(h, "h", dt, (S, H), x.device)
-    with _on(x, stream) as st:
-        if h is None:
-            h = torch.empty_like(x)
-        q = torch.empty((S, H), dtype=torch.float8_e4m3fn, device=x.device)
-        sc = torch.empty((S, -(-H // Q8_BLOCK)), dtype=torch.float8_e8m0fnu, device=x.device)
-        _check(lib().q3vl_add_rms_norm_q8(ctypes.byref(cfg), _ptr(x), _ptr(delta), S, _ptr(gain),
-                                          _ptr(h), _ptr(q), _ptr(sc), st))
+        if not _is(delta, dt, shape, index):
+            _arg(delta, "delta", (dt,), shape, x.device)
+        if h is not None and not _is(h, dt, shape, index):
+            _arg(h, "h", (dt,), shape, x.device)
+    return _run(x, stream, _add_rms_norm_q8, cfg, x, gain, delta, h)
+
+
+def _add_rms_norm_q8(cfg, x, gain, delta, h, st):
+    S, H = x.shape
+    if h is None:
+        h = torch.empty_like(x)
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    sc = x.new_empty((S, -(-H // Q8_BLOCK)), dtype=torch.float8_e8m0fnu)
+    _check(lib().q3vl_add_rms_norm_q8(
+        ctypes.byref(cfg), x.data_ptr(), None if delta is None else delta.data_ptr(), S,
+        None if gain is None else gain.data_ptr(), h.data_ptr(), q.data_ptr(), sc.data_ptr(), st))
     return h, q, sc
 
 
@@ -517,22 +540,28 @@ def linear_q8(xq: torch.Tensor, scales: torch.Tensor, lin: LinearQ8,
     N, K = lin.weight.shape
     if xq.dim() != 2 or xq.shape[1] != K:
         raise Q3VLError(_abi.EINVAL, f"xq must be [M, {K}], not {tuple(xq.shape)}")
-    M = xq.shape[0]
-    _arg(scales, "scales", (torch.float8_e8m0fnu,), (M, -(-K // Q8_BLOCK)), xq.device)
-    if lin.weight.device != xq.device:
+    M, index = xq.shape[0], xq.get_device()
+    if not _is(scales, torch.float8_e8m0fnu, (M, -(-K // Q8_BLOCK)), index):
+        _arg(scales, "scales", (torch.float8_e8m0fnu,), (M, -(-K // Q8_BLOCK)), xq.device)
+    if lin.weight.get_device() != index:
         raise Q3VLError(_abi.EINVAL, f"the weight is on {lin.weight.device}, xq on {xq.device}")
     if out_dtype not in _ROW_TYPES:
         raise Q3VLError(_abi.EUNSUPPORTED, f"out_dtype must be bfloat16 or float32, not {out_dtype}")
-    if resid is not None:
+    if resid is not None and not _is(resid, out_dtype, (M, N), index):
         _arg(resid, "resid", (out_dtype,), (M, N), xq.device)
-    if out is not None:
+    if out is not None and not _is(out, out_dtype, (M, N), index):
         _arg(out, "out", (out_dtype,), (M, N), xq.device)
-    with _on(xq, stream) as st:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=xq.device)
-        _check(lib().q3vl_linear_q8(
-            _ptr(xq), _ptr(scales), M, _ptr(lin.weight), _ptr(lin.scales), N, K, _ptr(resid),
-            _ptr(out), _abi.DTYPE_BF16 if out_dtype == torch.bfloat16 else _abi.DTYPE_FP32, st))
+    return _run(xq, stream, _linear_q8, xq, scales, lin, resid, out_dtype, out)
+
+
+def _linear_q8(xq, scales, lin, resid, out_dtype, out, st):
+    M, (N, K) = xq.shape[0], lin.weight.shape
+    if out is None:
+        out = xq.new_empty((M, N), dtype=out_dtype)
+    _check(lib().q3vl_linear_q8(
+        xq.data_ptr(), scales.data_ptr(), M, lin.weight.data_ptr(), lin.scales.data_ptr(), N, K,
+        None if resid is None else resid.data_ptr(), out.data_ptr(),
+        _abi.DTYPE_BF16 if out_dtype is torch.bfloat16 else _abi.DTYPE_FP32, st))
     return out
 
 
@@ -547,7 +576,8 @@ def _lm_head_q8(cfg, x_rows, final_norm, lin, logits, ws, stream):
         raise Q3VLError(_abi.EINVAL, f"the weight is on {lin.weight.device}, x_rows on {x_rows.device}")
     if logits is not None:
         _arg(logits, "logits", (torch.float32,), (B, vocab), x_rows.device)
-    with _on(x_rows, stream) as st:
+
+    def call(logits, ws, st):
         if logits is None:
             logits = torch.empty((B, vocab), dtype=torch.float32, device=x_rows.device)
         if ws is None:
@@ -558,11 +588,14 @@ def _lm_head_q8(cfg, x_rows, final_norm, lin, logits, ws, stream):
         _check(lib().q3vl_lm_head_q8(ctypes.byref(cfg), _ptr(x_rows), B, _ptr(final_norm),
                                      _ptr(lin.weight), _ptr(lin.scales), vocab, _ptr(logits),
                                      _ptr(ws), ws.numel(), st))
-    return logits
+        return logits
+    return _run(x_rows, stream, call, logits, ws)
 
 
 def _index(t: torch.Tensor, name: str, n: int, device) -> None:
-    _arg(t, name, (torch.int32,), (n,), device)
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == (n,) and
+            t.device == device and t.is_contiguous()):
+        _arg(t, name, (torch.int32,), (n,), device)
 
 
 def kv_store_q8(cfg: Config, k: torch.Tensor, v: torch.Tensor, kv: KvCacheQ8, seq: torch.Tensor,
@@ -575,27 +608,32 @@ def kv_store_q8(cfg: Config, k: torch.Tensor, v: torch.Tensor, kv: KvCacheQ8, se
     is not advanced.
     """
     dkv = cfg.n_kv_heads * cfg.head_dim
+    device = kv.k.device
     for t, name in ((k, "k"), (v, "v")):
         if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != dkv:
             raise Q3VLError(_abi.EINVAL, f"{name} must be bfloat16 [T, {dkv}], not "
                                          f"{t.dtype} {tuple(t.shape)}")
         if t.shape[0] > 0 and (t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < dkv)):
             raise Q3VLError(_abi.EINVAL, f"{name} must have contiguous rows that do not overlap")
-        if t.device != kv.k.device:
-            raise Q3VLError(_abi.EINVAL, f"{name} is on {t.device}, the cache on {kv.k.device}")
+        if t.device != device:
+            raise Q3VLError(_abi.EINVAL, f"{name} is on {t.device}, the cache on {device}")
     T, B = k.shape[0], seq.numel()
     if v.shape != k.shape or (T > 1 and v.stride(0) != k.stride(0)):
         raise Q3VLError(_abi.EINVAL, "k and v must have one shape and row stride")
     if kv.k.shape[2] != dkv:
         raise Q3VLError(_abi.EINVAL, f"the cache has rows of {kv.k.shape[2]}, the config {dkv}")
-    _index(seq, "seq", B, k.device)
-    _index(lens, "lens", B, k.device)
+    _index(seq, "seq", B, device)
+    _index(lens, "lens", B, device)
     if starts is not None:
-        _index(starts, "starts", B + 1, k.device)
+        _index(starts, "starts", B + 1, device)
     ld = k.stride(0) if T > 1 else dkv
-    with _on(k, stream) as st:
-        _check(lib().q3vl_kv_store_q8(ctypes.byref(cfg), _ptr(k), _ptr(v), ld, T, _ptr(starts), B,
-                                      ctypes.byref(kv.struct), _ptr(seq), _ptr(lens), st))
+    _run(k, stream, _kv_store_q8, cfg, k, v, ld, T, starts, B, kv, seq, lens)
+
+
+def _kv_store_q8(cfg, k, v, ld, T, starts, B, kv, seq, lens, st):
+    _check(lib().q3vl_kv_store_q8(ctypes.byref(cfg), k.data_ptr(), v.data_ptr(), ld, T,
+                                  None if starts is None else starts.data_ptr(), B,
+                                  ctypes.byref(kv.struct), seq.data_ptr(), lens.data_ptr(), st))
 
 
 def attention_q8_workspace(cfg: Config, B: int, cap: int, device="cuda") -> torch.Tensor:
@@ -617,20 +655,25 @@ def attention_q8(cfg: Config, q: torch.Tensor, kv: KvCacheQ8, seq: torch.Tensor,
     if kv.k.shape[2] != cfg.n_kv_heads * cfg.head_dim:
         raise Q3VLError(_abi.EINVAL, f"the cache has rows of {kv.k.shape[2]}, the config "
                                      f"{cfg.n_kv_heads * cfg.head_dim}")
-    if kv.k.device != q.device:
-        raise Q3VLError(_abi.EINVAL, f"the cache is on {kv.k.device}, q on {q.device}")
+    device = q.device
+    if kv.k.device != device:
+        raise Q3VLError(_abi.EINVAL, f"the cache is on {kv.k.device}, q on {device}")
     B = q.shape[0]
-    _index(seq, "seq", B, q.device)
-    _index(lens, "lens", B, q.device)
+    _index(seq, "seq", B, device)
+    _index(lens, "lens", B, device)
     if o is not None:
-        _arg(o, "o", (torch.bfloat16,), (B, dq), q.device)
-    with _on(q, stream) as st:
-        if o is None:
-            o = torch.empty_like(q)
-        if ws is None:
-            ws = attention_q8_workspace(cfg, B, kv.cap, q.device)
-        _check(lib().q3vl_attention_q8(ctypes.byref(cfg), _ptr(q), B, ctypes.byref(kv.struct),
-                                       _ptr(seq), _ptr(lens), _ptr(o), _ptr(ws), ws.numel(), st))
+        _arg(o, "o", (torch.bfloat16,), (B, dq), device)
+    return _run(q, stream, _attention_q8, cfg, q, B, kv, seq, lens, o, ws)
+
+
+def _attention_q8(cfg, q, B, kv, seq, lens, o, ws, st):
+    if o is None:
+        o = torch.empty_like(q)
+    if ws is None:
+        ws = attention_q8_workspace(cfg, B, kv.cap, q.device)
+    _check(lib().q3vl_attention_q8(ctypes.byref(cfg), q.data_ptr(), B, ctypes.byref(kv.struct),
+                                   seq.data_ptr(), lens.data_ptr(), o.data_ptr(), ws.data_ptr(),
+                                   ws.numel(), st))
     return o
 
 
