@@ -117,6 +117,25 @@ cudaError_t max_active_clusters(const void* kernel, int threads, size_t smem, in
   return cudaSuccess;
 }
 
+cudaError_t max_active_blocks(const void* kernel, int threads, int* out) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int>, int> cache;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_tuple(kernel, dev, threads);
+  auto it = cache.find(key);
+  if (it == cache.end()) {
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);
+    if (e != cudaSuccess) return e;
+    it = cache.emplace(key, n).first;
+  }
+  *out = it->second;
+  return cudaSuccess;
+}
+
 WsLayout ws_layout(const q3vl_config& c, int64_t S) {
   WsLayout L;
   const size_t e = elem_bytes(c);

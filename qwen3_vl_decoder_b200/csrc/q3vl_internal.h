@@ -288,6 +288,8 @@ cudaError_t allow_nonportable_clusters(const void* kernel);
 // at once; cached per (kernel, device) under a lock.
 cudaError_t max_active_clusters(const void* kernel, int threads, size_t smem, int cluster,
                                 int* out);
+// Blocks of `threads` threads (no dynamic shared memory) that one SM holds at once (cached).
+cudaError_t max_active_blocks(const void* kernel, int threads, int* out);
 
 // Adds n to the process-wide count of kernels this library enqueued and
 // returns the launch status of the last one.

@@ -39,12 +39,15 @@ __device__ __forceinline__ float finite_abs(float x) {
 // Four floats (already divided by the scale) to e4m3, round to nearest even,
 // element 0 in the low byte. fma(x, 0, x) turns an infinity into NaN (the
 // conversion alone would saturate it) and leaves finite values as they are.
-__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
-  a = fmaf(a, 0.f, a); b = fmaf(b, 0.f, b); c = fmaf(c, 0.f, c); d = fmaf(d, 0.f, d);
+// pack_e4m3x4_finite is for values without infinities.
+__device__ __forceinline__ uint32_t pack_e4m3x4_finite(float a, float b, float c, float d) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  return pack_e4m3x4_finite(fmaf(a, 0.f, a), fmaf(b, 0.f, b), fmaf(c, 0.f, c), fmaf(d, 0.f, d));
 }
 
 // Four e4m3 bytes to floats.

@@ -6,76 +6,123 @@
 namespace q3vl {
 namespace {
 
+// Eight elements of a row as loaded.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+    load8(reinterpret_cast<const T*>(v), f);
+  }
+};
+
 // ---------------------------------------------------------------------------
 // h = x + delta; y = h * (1 / rms(h)) * gain; e4m3 of y, a scale per 128
-// columns. One block per row; a thread takes units of 8 columns, so 16
-// neighbouring threads hold one block of 128 and its maximum is four shuffles.
-// The row stays in registers between the sum of squares (fp32) and the
-// rounding: every input is read once. Bound by memory: 7 bytes per bf16
-// element with a delta (3 without).
+// columns. A block takes rows blockIdx.x, + gridDim.x, ...; a thread takes
+// units of 8 columns, so 16 neighbouring threads hold one block of 128 and its
+// maximum is four shuffles. The row stays in registers between the sum of
+// squares (fp32) and the rounding: every input is read once. Bound by memory:
+// 7 bytes per bf16 element with a delta (3 without). Rows up to 8192 wide (NV =
+// 1) go through as many blocks as fit, which request the next row before they
+// reduce this one; that wants 48 registers, for three quarters of the threads.
+// Measured, against a block per row without: bf16 with a delta 4096 x 2560 14.9
+// us (16.5), 8192 x 5120 53 (67, 5.5 TB/s); fp32 2129 x 5120 12.7 (15.4).
 // ---------------------------------------------------------------------------
-template <typename T, int NV>
-__global__ void __launch_bounds__(1024)
+template <typename T, int NV, bool PRE, bool DELTA>
+__global__ void __maxnreg__(NV == 1 ? 48 : 64)
 add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t* q,
-                       uint8_t* scales, int width, int nblk, float eps) {
+                       uint8_t* scales, int64_t rows, int width, int nblk, float eps) {
   const int t = threadIdx.x, lane = t & 31;
-  const int64_t row = blockIdx.x;
   const int units = width / 8;
-  const T* xr = x + row * width;
+  __shared__ float s_ss[2][32];
   griddep_launch_dependents();
   griddep_wait();
-  float f[NV][8];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int u = t + i * blockDim.x;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
+  Raw8<T> xn, dn, gn;
+  auto request = [&](int64_t row, int u) {
+    xn.zero();
+    dn.zero();
     if (u < units) {
-      load8(xr + 8 * u, f[i]);
-      if (delta != nullptr) {
+      xn.load(x + row * width + 8 * u);
+      if (DELTA) dn.load(delta + row * width + 8 * u);
+    }
+  };
+  auto request_gain = [&](int u) {
+    gn.zero();
+    if (gain != nullptr && u < units) gn.load(gain + 8 * u);
+  };
+  if (PRE) request(blockIdx.x, t);
+  if (NV == 1) request_gain(t);
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
+    float f[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int u = t + i * blockDim.x;
+      if (!PRE) request(row, u);
+      xn.floats(f[i]);
+      if (DELTA) {
         float d[8];
-        load8(delta + row * width + 8 * u, d);
+        dn.floats(d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[i][j] += d[j];
-        store8(h + row * width + 8 * u, f[i]);
+        if (u < units) store8(h + row * width + 8 * u, f[i]);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
+    }
+    if (PRE && row + gridDim.x < rows) request(row + gridDim.x, t);
+    float inv = 1.f;
+    if (gain != nullptr) {
+      ss = warp_sum(ss);
+      if (lane == 0) s_ss[par][t >> 5] = ss;
+      __syncthreads();
+      ss = lane < (blockDim.x >> 5) ? s_ss[par][lane] : 0.f;
+      ss = warp_sum(ss);
+      inv = 1.0f / sqrtf(ss / static_cast<float>(width) + eps);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
-  }
-  float inv = 1.f;
-  if (gain != nullptr) {
-    __shared__ float s_ss[32];
-    ss = warp_sum(ss);
-    if (lane == 0) s_ss[t >> 5] = ss;
-    __syncthreads();
-    ss = lane < (blockDim.x >> 5) ? s_ss[lane] : 0.f;
-    ss = warp_sum(ss);
-    inv = 1.0f / sqrtf(ss / static_cast<float>(width) + eps);
-  }
+    for (int i = 0; i < NV; ++i) {
+      const int u = t + i * blockDim.x;
+      if (NV > 1) request_gain(u);
+      if (gain != nullptr) {
+        float g[8];
+        gn.floats(g);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int u = t + i * blockDim.x;
-    if (gain != nullptr && u < units) {
-      float g[8];
-      load8(gain + 8 * u, g);
+        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * inv * g[j];
+      }
+      float a = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * inv * g[j];
-    }
-    float a = 0.f;
+      for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(f[i][j]));  // leaves NaN out
+      const bool infinite = __any_sync(0xffffffffu, a == INFINITY);
+      if (infinite) {
+        a = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(f[i][j]));
+        for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(f[i][j]));
+      }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const uint32_t e = e8m0_of_amax(a);
-    const float s = e8m0_inverse(e);
-    if (u < units) {
-      uint2 w;
-      w.x = pack_e4m3x4(f[i][0] * s, f[i][1] * s, f[i][2] * s, f[i][3] * s);
-      w.y = pack_e4m3x4(f[i][4] * s, f[i][5] * s, f[i][6] * s, f[i][7] * s);
-      *reinterpret_cast<uint2*>(q + row * width + 8 * u) = w;
-      if ((t & 15) == 0) scales[row * nblk + u / 16] = static_cast<uint8_t>(e);
+      for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      const uint32_t e = e8m0_of_amax(a);
+      const float s = e8m0_inverse(e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[i][j] *= s;
+        if (infinite) f[i][j] = fmaf(f[i][j], 0.f, f[i][j]);
+      }
+      if (u < units) {
+        uint2 w;
+        w.x = pack_e4m3x4_finite(f[i][0], f[i][1], f[i][2], f[i][3]);
+        w.y = pack_e4m3x4_finite(f[i][4], f[i][5], f[i][6], f[i][7]);
+        *reinterpret_cast<uint2*>(q + row * width + 8 * u) = w;
+        if ((t & 15) == 0) scales[row * nblk + u / 16] = static_cast<uint8_t>(e);
+      }
     }
   }
 }
@@ -150,7 +197,7 @@ struct StoreQ8Params {
   int32_t* err;
 };
 
-__global__ void __launch_bounds__(256) kv_store_q8_kernel(StoreQ8Params p) {
+__global__ void __launch_bounds__(256, 4) kv_store_q8_kernel(StoreQ8Params p) {
   const int t = threadIdx.x, lane = t & 31;
   __shared__ int s_item[4];  // slot (-1: none), rows cached, first source row, rows
   __shared__ int s_blk;
@@ -196,18 +243,26 @@ __global__ void __launch_bounds__(256) kv_store_q8_kernel(StoreQ8Params p) {
   uint8_t* scale = (blockIdx.z == 0 ? p.ks : p.vs) + (int64_t(slot) * nblk + blk) * p.nkv + g;
   const int lo = max(len, blk * 128), hi = min(len + n, blk * 128 + 128);
   const int64_t s0 = int64_t(s_item[2]) + (lo - len);
-  float f[8][8];
-  float a = 0.f;
+  Raw8<__nv_bfloat16> f[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = (t >> 4) + 16 * i;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
-    if (lo + r < hi && dcheck(s0 + r < p.T, p.err, kWhereDbgQ8)) load8(src + (s0 + r) * p.ld, f[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(f[i][j]));
+    f[i].zero();
+    if (lo + r < hi && dcheck(s0 + r < p.T, p.err, kWhereDbgQ8)) f[i].load(src + (s0 + r) * p.ld);
   }
-  a = warp_max(a);
+  // the magnitudes of two bf16 to a word compare as integers; 0x7f80 and above
+  // are not finite
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w[4] = {f[i].v[0].x, f[i].v[0].y, f[i].v[0].z, f[i].v[0].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t m = w[j] & 0x7fff7fffu;
+      top = __vmaxu2(top, m & __vcmpltu2(m, 0x7f807f80u));
+    }
+  }
+  float a = warp_max(fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u)));
   if (lane == 0) s_a[t >> 5] = a;
   const bool keeps = blk * 128 < len;  // the block holds earlier rows
   const uint32_t was = keeps ? *scale : 0u;
@@ -236,9 +291,11 @@ __global__ void __launch_bounds__(256) kv_store_q8_kernel(StoreQ8Params p) {
   for (int i = 0; i < 8; ++i) {
     const int r = lo + (t >> 4) + 16 * i;
     if (r < hi && dcheck(r < p.cap, p.err, kWhereDbgQ8)) {
+      float v[8];
+      f[i].floats(v);
       uint2 w;
-      w.x = pack_e4m3x4(f[i][0] * s, f[i][1] * s, f[i][2] * s, f[i][3] * s);
-      w.y = pack_e4m3x4(f[i][4] * s, f[i][5] * s, f[i][6] * s, f[i][7] * s);
+      w.x = pack_e4m3x4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+      w.y = pack_e4m3x4(v[4] * s, v[5] * s, v[6] * s, v[7] * s);
       *reinterpret_cast<uint2*>(dst + int64_t(r) * rs) = w;
     }
   }
@@ -256,17 +313,30 @@ cudaError_t launch_norm_t(const void* x, const void* delta, int64_t S, const voi
                           uint8_t* q, uint8_t* scales, int width, float eps, cudaStream_t st) {
   const int units = width / 8;
   const int nblk = (width + kQ8Block - 1) / kQ8Block;
-  auto go = [&](auto kern, int nv) {
+  auto go = [&](auto kern, int nv, bool pre) {
     const int th = ((units + nv - 1) / nv + 31) / 32 * 32;
-    return launch_pdl_plain(kern, dim3(static_cast<unsigned>(S)), dim3(th), 0, st,
+    int64_t blocks = S;
+    if (pre) {
+      int n = 0;
+      const cudaError_t e = max_active_blocks(reinterpret_cast<const void*>(kern), th, &n);
+      if (e != cudaSuccess) return e;
+      const int64_t fit = int64_t(sm_count()) * (n > 0 ? n : 1);
+      if (blocks > fit) blocks = fit;
+    }
+    return launch_pdl_plain(kern, dim3(static_cast<unsigned>(blocks)), dim3(th), 0, st,
                             static_cast<const T*>(x), static_cast<const T*>(delta),
-                            static_cast<const T*>(gain), static_cast<T*>(h), q, scales, width,
+                            static_cast<const T*>(gain), static_cast<T*>(h), q, scales, S, width,
                             nblk, eps);
   };
   cudaError_t e;
-  if (units <= 1024) e = go(add_rms_norm_q8_kernel<T, 1>, 1);
-  else if (units <= 4096) e = go(add_rms_norm_q8_kernel<T, 4>, 4);
-  else return cudaErrorInvalidValue;
+  if (units <= 1024)
+    e = delta != nullptr ? go(add_rms_norm_q8_kernel<T, 1, true, true>, 1, true)
+                         : go(add_rms_norm_q8_kernel<T, 1, true, false>, 1, true);
+  else if (units <= 4096)
+    e = delta != nullptr ? go(add_rms_norm_q8_kernel<T, 4, false, true>, 4, false)
+                         : go(add_rms_norm_q8_kernel<T, 4, false, false>, 4, false);
+  else
+    return cudaErrorInvalidValue;
   if (e != cudaSuccess) return e;
   return counted_launch(1);
 }
