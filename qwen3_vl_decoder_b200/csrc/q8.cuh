@@ -60,6 +60,12 @@ __device__ __forceinline__ float4 unpack_e4m3x4(uint32_t w) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Eight consecutive elements of a row as floats (16-byte aligned address).
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
   const uint4 v = *reinterpret_cast<const uint4*>(p);

@@ -21,6 +21,13 @@ struct Raw8 {
   __device__ __forceinline__ void floats(float (&f)[8]) const {
     load8(reinterpret_cast<const T*>(v), f);
   }
+  // the same as four pairs for the packed arithmetic
+  __device__ __forceinline__ void pairs(uint64_t (&f)[4]) const {
+    float s[8];
+    floats(s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = f2_pack(s[2 * j], s[2 * j + 1]);
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -32,8 +39,9 @@ struct Raw8 {
 // 7 bytes per bf16 element with a delta (3 without). Rows up to 8192 wide (NV =
 // 1) go through as many blocks as fit, which request the next row before they
 // reduce this one; that wants 48 registers, for three quarters of the threads.
-// Measured, against a block per row without: bf16 with a delta 4096 x 2560 14.9
-// us (16.5), 8192 x 5120 53 (67, 5.5 TB/s); fp32 2129 x 5120 12.7 (15.4).
+// Measured, against a block per row without: bf16 with a delta 4096 x 2560 16.2
+// us (18.2), 8192 x 5120 58 (75, 5.1 TB/s); fp32 2129 x 5120 14.4 (19.3). Rows on
+// their way in a ring of bulk copies instead of registers: 18.9 us at the first.
 // ---------------------------------------------------------------------------
 template <typename T, int NV, bool PRE, bool DELTA>
 __global__ void __maxnreg__(NV == 1 ? 48 : 64)
@@ -61,65 +69,90 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
   if (NV == 1) request_gain(t);
   int par = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
-    float f[NV][8];
-    float ss = 0.f;
+    uint64_t f[NV][4];  // two elements each: packed fp32 arithmetic
+    uint64_t ss2 = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int u = t + i * blockDim.x;
       if (!PRE) request(row, u);
-      xn.floats(f[i]);
+      xn.pairs(f[i]);
       if (DELTA) {
-        float d[8];
-        dn.floats(d);
+        uint64_t d[4];
+        dn.pairs(d);
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] += d[j];
-        if (u < units) store8(h + row * width + 8 * u, f[i]);
+        for (int j = 0; j < 4; ++j) f2_unpack(f2_add(f[i][j], d[j]), v[2 * j], v[2 * j + 1]);
+        if (u < units) store8(h + row * width + 8 * u, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i][j] = f2_pack(v[2 * j], v[2 * j + 1]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
+      for (int j = 0; j < 4; ++j) ss2 = f2_fma(f[i][j], f[i][j], ss2);
     }
     if (PRE && row + gridDim.x < rows) request(row + gridDim.x, t);
-    float inv = 1.f;
+    float inv = 1.f, inv_lo = 0.f;  // 1 / rms in two parts
     if (gain != nullptr) {
-      ss = warp_sum(ss);
+      float ss, ss1;
+      f2_unpack(ss2, ss, ss1);
+      ss = warp_sum(ss + ss1);
       if (lane == 0) s_ss[par][t >> 5] = ss;
       __syncthreads();
       ss = lane < (blockDim.x >> 5) ? s_ss[par][lane] : 0.f;
       ss = warp_sum(ss);
-      inv = 1.0f / sqrtf(ss / static_cast<float>(width) + eps);
+      const float var = ss / static_cast<float>(width) + eps;
+      inv = 1.0f / sqrtf(var);
+      // var inv^2 = 1 - d, so 1 / sqrt(var) = inv (1 + d / 2)
+      const float a = var * inv, b = fmaf(var, inv, -a);
+      inv_lo = 0.5f * inv * (fmaf(-a, inv, 1.f) - b * inv);
+      if (!(fabsf(inv_lo) < inv)) inv_lo = 0.f;  // var 0 or not finite
     }
+    const uint64_t inv2 = f2_pack(inv, inv), minus2 = f2_pack(-inv, -inv),
+                   lo2 = f2_pack(inv_lo, inv_lo);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int u = t + i * blockDim.x;
       if (NV > 1) request_gain(u);
       if (gain != nullptr) {
-        float g[8];
-        gn.floats(g);
+        uint64_t g[4];
+        gn.pairs(g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * inv * g[j];
+        for (int j = 0; j < 4; ++j) {
+          // f * inv * g rounded once: about one value in a million lies so
+          // near a border of e4m3 that an error in the last place turns it
+          // over (rounding f * inv as well is 1.3 us faster at 4096 x 2560 and
+          // turns over two to three times as many)
+          const uint64_t y = f2_mul(f[i][j], inv2);
+          const uint64_t rest = f2_fma(f[i][j], lo2, f2_fma(f[i][j], inv2, f2_mul(f[i][j], minus2)));
+          f[i][j] = f2_fma(y, g[j], f2_mul(rest, g[j]));
+        }
       }
-      float a = 0.f;
+      float v[8], a = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(f[i][j]));  // leaves NaN out
+      for (int j = 0; j < 4; ++j) {
+        f2_unpack(f[i][j], v[2 * j], v[2 * j + 1]);
+        a = fmaxf(a, fmaxf(fabsf(v[2 * j]), fabsf(v[2 * j + 1])));  // leaves NaN out
+      }
       const bool infinite = __any_sync(0xffffffffu, a == INFINITY);
       if (infinite) {
         a = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(f[i][j]));
+        for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(v[j]));
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
       const uint32_t e = e8m0_of_amax(a);
       const float s = e8m0_inverse(e);
+      const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[i][j] *= s;
-        if (infinite) f[i][j] = fmaf(f[i][j], 0.f, f[i][j]);
+      for (int j = 0; j < 4; ++j) f2_unpack(f2_mul(f[i][j], s2), v[2 * j], v[2 * j + 1]);
+      if (infinite) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], 0.f, v[j]);
       }
       if (u < units) {
         uint2 w;
-        w.x = pack_e4m3x4_finite(f[i][0], f[i][1], f[i][2], f[i][3]);
-        w.y = pack_e4m3x4_finite(f[i][4], f[i][5], f[i][6], f[i][7]);
+        w.x = pack_e4m3x4_finite(v[0], v[1], v[2], v[3]);
+        w.y = pack_e4m3x4_finite(v[4], v[5], v[6], v[7]);
         *reinterpret_cast<uint2*>(q + row * width + 8 * u) = w;
         if ((t & 15) == 0) scales[row * nblk + u / 16] = static_cast<uint8_t>(e);
       }
