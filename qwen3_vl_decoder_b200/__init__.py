@@ -246,10 +246,7 @@ class KvCacheQ8:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.struct = KvCacheQ8Struct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                                       v_scale.data_ptr(), cap, n_seq)
-
-    @property
-    def cap(self) -> int:
-        return int(self.struct.cap)
+        self.cap, self._width, self._index = cap, dkv, k.get_device()
 
 
 def kv_caches(cfg: Config, n_layers: int, n_seq: int, cap: int, device="cuda",
@@ -423,11 +420,15 @@ def _is(t, dtype, shape, index: int) -> bool:
             t.get_device() == index and t.is_contiguous())
 
 
-def _run(t: torch.Tensor, stream, call, *args):
-    """call(*args, stream handle) with t's device current (the library works on the current one)
-    and, where a stream is given, with it current, so that what `call` allocates belongs to it."""
-    if stream is None and t.is_cuda and t.get_device() == torch._C._cuda_getDevice():
-        return call(*args, torch._C._cuda_getCurrentRawStream(t.get_device()))
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _run(t: torch.Tensor, index: int, stream, call, *args):
+    """call(*args, stream handle) with t's device current (`index`; the library works on the
+    current one) and, where a stream is given, with it current, so that what `call` allocates
+    belongs to it."""
+    if stream is None and index >= 0 and index == _device():
+        return call(*args, _raw_stream(index))
     with _on(t, stream) as st:
         return call(*args, st)
 
@@ -467,6 +468,7 @@ class LinearQ8:
         _arg(scales, "scales", (torch.float8_e8m0fnu,), (-(-N // Q8_BLOCK), -(-K // Q8_BLOCK)),
              weight.device)
         self.weight, self.scales = weight, scales
+        self._index = weight.get_device()
 
     @property
     def shape(self) -> Tuple[int, int]:
@@ -488,7 +490,7 @@ def quantize_weight_q8(w: torch.Tensor, stream=None) -> LinearQ8:
         _check(lib().q3vl_quantize_weight_q8(ctypes.byref(cfg), _ptr(w), N, K, _ptr(wq), _ptr(ws),
                                              st))
         return LinearQ8(wq, ws)
-    return _run(w, stream, call)
+    return _run(w, w.get_device(), stream, call)
 
 
 def add_rms_norm_q8(cfg: Config, x: torch.Tensor, gain: Optional[torch.Tensor],
@@ -501,10 +503,11 @@ def add_rms_norm_q8(cfg: Config, x: torch.Tensor, gain: Optional[torch.Tensor],
     tensor by default.
     """
     dt = torch_dtype(cfg)
-    _arg(x, "x", (dt,))
-    if x.dim() != 2 or x.shape[1] != cfg.hidden:
-        raise Q3VLError(_abi.EINVAL, f"x must be [S, {cfg.hidden}], not {tuple(x.shape)}")
+    if not (isinstance(x, torch.Tensor) and x.dtype is dt and x.is_contiguous()):
+        _arg(x, "x", (dt,))
     shape, index = x.shape, x.get_device()
+    if len(shape) != 2 or shape[1] != cfg.hidden:
+        raise Q3VLError(_abi.EINVAL, f"x must be [S, {cfg.hidden}], not {tuple(x.shape)}")
     if gain is not None and not _is(gain, dt, shape[1:], index):
         _arg(gain, "gain", (dt,), shape[1:], x.device)
     if delta is None:
@@ -516,7 +519,7 @@ def add_rms_norm_q8(cfg: Config, x: torch.Tensor, gain: Optional[torch.Tensor],
             _arg(delta, "delta", (dt,), shape, x.device)
         if h is not None and not _is(h, dt, shape, index):
             _arg(h, "h", (dt,), shape, x.device)
-    return _run(x, stream, _add_rms_norm_q8, cfg, x, gain, delta, h)
+    return _run(x, index, stream, _add_rms_norm_q8, cfg, x, gain, delta, h)
 
 
 def _add_rms_norm_q8(cfg, x, gain, delta, h, st):
@@ -525,9 +528,11 @@ def _add_rms_norm_q8(cfg, x, gain, delta, h, st):
         h = torch.empty_like(x)
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     sc = x.new_empty((S, -(-H // Q8_BLOCK)), dtype=torch.float8_e8m0fnu)
-    _check(lib().q3vl_add_rms_norm_q8(
+    rc = lib().q3vl_add_rms_norm_q8(
         ctypes.byref(cfg), x.data_ptr(), None if delta is None else delta.data_ptr(), S,
-        None if gain is None else gain.data_ptr(), h.data_ptr(), q.data_ptr(), sc.data_ptr(), st))
+        None if gain is None else gain.data_ptr(), h.data_ptr(), q.data_ptr(), sc.data_ptr(), st)
+    if rc:
+        _check(rc)
     return h, q, sc
 
 
@@ -536,14 +541,17 @@ def linear_q8(xq: torch.Tensor, scales: torch.Tensor, lin: LinearQ8,
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """[M, N] = x W^T (+ resid) of 8-bit rows (as add_rms_norm_q8 gives them) and an 8-bit
     weight, summed in fp32 and rounded once to out_dtype (bfloat16 or float32)."""
-    _arg(xq, "xq", (torch.float8_e4m3fn,))
+    if not (isinstance(xq, torch.Tensor) and xq.dtype is torch.float8_e4m3fn and
+            xq.is_contiguous()):
+        _arg(xq, "xq", (torch.float8_e4m3fn,))
     N, K = lin.weight.shape
-    if xq.dim() != 2 or xq.shape[1] != K:
+    shape, index = xq.shape, xq.get_device()
+    if len(shape) != 2 or shape[1] != K:
         raise Q3VLError(_abi.EINVAL, f"xq must be [M, {K}], not {tuple(xq.shape)}")
-    M, index = xq.shape[0], xq.get_device()
+    M = shape[0]
     if not _is(scales, torch.float8_e8m0fnu, (M, -(-K // Q8_BLOCK)), index):
         _arg(scales, "scales", (torch.float8_e8m0fnu,), (M, -(-K // Q8_BLOCK)), xq.device)
-    if lin.weight.get_device() != index:
+    if lin._index != index:
         raise Q3VLError(_abi.EINVAL, f"the weight is on {lin.weight.device}, xq on {xq.device}")
     if out_dtype not in _ROW_TYPES:
         raise Q3VLError(_abi.EUNSUPPORTED, f"out_dtype must be bfloat16 or float32, not {out_dtype}")
@@ -551,17 +559,18 @@ def linear_q8(xq: torch.Tensor, scales: torch.Tensor, lin: LinearQ8,
         _arg(resid, "resid", (out_dtype,), (M, N), xq.device)
     if out is not None and not _is(out, out_dtype, (M, N), index):
         _arg(out, "out", (out_dtype,), (M, N), xq.device)
-    return _run(xq, stream, _linear_q8, xq, scales, lin, resid, out_dtype, out)
+    return _run(xq, index, stream, _linear_q8, xq, scales, lin, resid, out_dtype, out, M, N, K)
 
 
-def _linear_q8(xq, scales, lin, resid, out_dtype, out, st):
-    M, (N, K) = xq.shape[0], lin.weight.shape
+def _linear_q8(xq, scales, lin, resid, out_dtype, out, M, N, K, st):
     if out is None:
         out = xq.new_empty((M, N), dtype=out_dtype)
-    _check(lib().q3vl_linear_q8(
+    rc = lib().q3vl_linear_q8(
         xq.data_ptr(), scales.data_ptr(), M, lin.weight.data_ptr(), lin.scales.data_ptr(), N, K,
         None if resid is None else resid.data_ptr(), out.data_ptr(),
-        _abi.DTYPE_BF16 if out_dtype is torch.bfloat16 else _abi.DTYPE_FP32, st))
+        _abi.DTYPE_BF16 if out_dtype is torch.bfloat16 else _abi.DTYPE_FP32, st)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -589,13 +598,12 @@ def _lm_head_q8(cfg, x_rows, final_norm, lin, logits, ws, stream):
                                      _ptr(lin.weight), _ptr(lin.scales), vocab, _ptr(logits),
                                      _ptr(ws), ws.numel(), st))
         return logits
-    return _run(x_rows, stream, call, logits, ws)
+    return _run(x_rows, x_rows.get_device(), stream, call, logits, ws)
 
 
-def _index(t: torch.Tensor, name: str, n: int, device) -> None:
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == (n,) and
-            t.device == device and t.is_contiguous()):
-        _arg(t, name, (torch.int32,), (n,), device)
+def _ints(t: torch.Tensor, name: str, n: int, kv: KvCacheQ8) -> None:
+    if not _is(t, torch.int32, (n,), kv._index):
+        _arg(t, name, (torch.int32,), (n,), kv.k.device)
 
 
 def kv_store_q8(cfg: Config, k: torch.Tensor, v: torch.Tensor, kv: KvCacheQ8, seq: torch.Tensor,
@@ -607,33 +615,45 @@ def kv_store_q8(cfg: Config, k: torch.Tensor, v: torch.Tensor, kv: KvCacheQ8, se
     ranges of a QKV buffer. seq (distinct slots) and lens: int32 [B]; starts: int32 [B+1]. lens
     is not advanced.
     """
-    dkv = cfg.n_kv_heads * cfg.head_dim
-    device = kv.k.device
+    dkv, index = cfg.n_kv_heads * cfg.head_dim, kv._index
+    shape, strides = k.shape, k.stride()
+    T, B = shape[0], seq.numel()
+    # rows of dkv elements, one shape, type, stride and device
+    if not (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and
+            len(shape) == 2 and shape[1] == dkv and v.shape == shape and strides[1] == 1 and
+            strides[0] >= dkv and v.stride() == strides and k.get_device() == index and
+            v.get_device() == index):
+        _kv_rows(k, v, dkv, kv)
+    if kv._width != dkv:
+        raise Q3VLError(_abi.EINVAL, f"the cache has rows of {kv._width}, the config {dkv}")
+    _ints(seq, "seq", B, kv)
+    _ints(lens, "lens", B, kv)
+    if starts is not None:
+        _ints(starts, "starts", B + 1, kv)
+    ld = strides[0] if T > 1 else dkv
+    _run(k, index, stream, _kv_store_q8, cfg, k, v, ld, T, starts, B, kv, seq, lens)
+
+
+def _kv_rows(k, v, dkv, kv) -> None:
+    """What kv_store_q8 asks of k and v, one by one (a single row may have any stride)."""
     for t, name in ((k, "k"), (v, "v")):
         if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != dkv:
             raise Q3VLError(_abi.EINVAL, f"{name} must be bfloat16 [T, {dkv}], not "
                                          f"{t.dtype} {tuple(t.shape)}")
         if t.shape[0] > 0 and (t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < dkv)):
             raise Q3VLError(_abi.EINVAL, f"{name} must have contiguous rows that do not overlap")
-        if t.device != device:
-            raise Q3VLError(_abi.EINVAL, f"{name} is on {t.device}, the cache on {device}")
-    T, B = k.shape[0], seq.numel()
-    if v.shape != k.shape or (T > 1 and v.stride(0) != k.stride(0)):
+        if t.device != kv.k.device:
+            raise Q3VLError(_abi.EINVAL, f"{name} is on {t.device}, the cache on {kv.k.device}")
+    if v.shape != k.shape or (k.shape[0] > 1 and v.stride(0) != k.stride(0)):
         raise Q3VLError(_abi.EINVAL, "k and v must have one shape and row stride")
-    if kv.k.shape[2] != dkv:
-        raise Q3VLError(_abi.EINVAL, f"the cache has rows of {kv.k.shape[2]}, the config {dkv}")
-    _index(seq, "seq", B, device)
-    _index(lens, "lens", B, device)
-    if starts is not None:
-        _index(starts, "starts", B + 1, device)
-    ld = k.stride(0) if T > 1 else dkv
-    _run(k, stream, _kv_store_q8, cfg, k, v, ld, T, starts, B, kv, seq, lens)
 
 
 def _kv_store_q8(cfg, k, v, ld, T, starts, B, kv, seq, lens, st):
-    _check(lib().q3vl_kv_store_q8(ctypes.byref(cfg), k.data_ptr(), v.data_ptr(), ld, T,
-                                  None if starts is None else starts.data_ptr(), B,
-                                  ctypes.byref(kv.struct), seq.data_ptr(), lens.data_ptr(), st))
+    rc = lib().q3vl_kv_store_q8(ctypes.byref(cfg), k.data_ptr(), v.data_ptr(), ld, T,
+                                None if starts is None else starts.data_ptr(), B,
+                                ctypes.byref(kv.struct), seq.data_ptr(), lens.data_ptr(), st)
+    if rc:
+        _check(rc)
 
 
 def attention_q8_workspace(cfg: Config, B: int, cap: int, device="cuda") -> torch.Tensor:
@@ -648,22 +668,22 @@ def attention_q8(cfg: Config, q: torch.Tensor, kv: KvCacheQ8, seq: torch.Tensor,
                  ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """o [B, nh*128] bf16: the attention of query row b (q [B, nh*128] bf16) over rows
     0..lens[b]-1 of slot seq[b] of an 8-bit cache; a length of 0 gives a zero row."""
-    dq = cfg.n_heads * cfg.head_dim
-    _arg(q, "q", (torch.bfloat16,))
-    if q.dim() != 2 or q.shape[1] != dq:
+    dq, dkv = cfg.n_heads * cfg.head_dim, cfg.n_kv_heads * cfg.head_dim
+    if not (isinstance(q, torch.Tensor) and q.dtype is torch.bfloat16 and q.is_contiguous()):
+        _arg(q, "q", (torch.bfloat16,))
+    shape, index = q.shape, q.get_device()
+    if len(shape) != 2 or shape[1] != dq:
         raise Q3VLError(_abi.EINVAL, f"q must be [B, {dq}], not {tuple(q.shape)}")
-    if kv.k.shape[2] != cfg.n_kv_heads * cfg.head_dim:
-        raise Q3VLError(_abi.EINVAL, f"the cache has rows of {kv.k.shape[2]}, the config "
-                                     f"{cfg.n_kv_heads * cfg.head_dim}")
-    device = q.device
-    if kv.k.device != device:
-        raise Q3VLError(_abi.EINVAL, f"the cache is on {kv.k.device}, q on {device}")
-    B = q.shape[0]
-    _index(seq, "seq", B, device)
-    _index(lens, "lens", B, device)
-    if o is not None:
-        _arg(o, "o", (torch.bfloat16,), (B, dq), device)
-    return _run(q, stream, _attention_q8, cfg, q, B, kv, seq, lens, o, ws)
+    if kv._width != dkv:
+        raise Q3VLError(_abi.EINVAL, f"the cache has rows of {kv._width}, the config {dkv}")
+    if kv._index != index:
+        raise Q3VLError(_abi.EINVAL, f"the cache is on {kv.k.device}, q on {q.device}")
+    B = shape[0]
+    _ints(seq, "seq", B, kv)
+    _ints(lens, "lens", B, kv)
+    if o is not None and not _is(o, torch.bfloat16, shape, index):
+        _arg(o, "o", (torch.bfloat16,), (B, dq), q.device)
+    return _run(q, index, stream, _attention_q8, cfg, q, B, kv, seq, lens, o, ws)
 
 
 def _attention_q8(cfg, q, B, kv, seq, lens, o, ws, st):
@@ -671,9 +691,11 @@ def _attention_q8(cfg, q, B, kv, seq, lens, o, ws, st):
         o = torch.empty_like(q)
     if ws is None:
         ws = attention_q8_workspace(cfg, B, kv.cap, q.device)
-    _check(lib().q3vl_attention_q8(ctypes.byref(cfg), q.data_ptr(), B, ctypes.byref(kv.struct),
-                                   seq.data_ptr(), lens.data_ptr(), o.data_ptr(), ws.data_ptr(),
-                                   ws.numel(), st))
+    rc = lib().q3vl_attention_q8(ctypes.byref(cfg), q.data_ptr(), B, ctypes.byref(kv.struct),
+                                 seq.data_ptr(), lens.data_ptr(), o.data_ptr(), ws.data_ptr(),
+                                 ws.numel(), st)
+    if rc:
+        _check(rc)
     return o
 
 
