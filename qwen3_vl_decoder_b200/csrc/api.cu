@@ -448,7 +448,7 @@ int run_layer(const q3vl_config& c, const q3vl_layer& w, void* x, int64_t S, cha
   if (kv8 != nullptr) {
     const char* k = static_cast<const char*>(qkv) + q_dim(c) * 2;
     Q3VL_CUDA(launch_kv_store_q8(c, k, k + kv_dim(c) * 2, qkv_dim(c), S, nullptr, 1, *kv8, nullptr,
-                                 nullptr, kv_seq, st),
+                                 nullptr, kv_seq, false, st),
               "8-bit kv cache store");
   }
   stage_event(3, st);
@@ -640,7 +640,7 @@ int run_decode_layer(const q3vl_config& c, const q3vl_layer& w, void* x, int32_t
     a.len = reinterpret_cast<const int32_t*>(ws + L8->zero);
     Q3VL_CUDA(launch_decode_gemm(Epi::kQkv, a, st), "decode qkv projection");
     Q3VL_CUDA(launch_kv_store_q8(c, ws + L8->k_new, ws + L8->v_new, kv_dim(c), B, nullptr, B, *kv8,
-                                 seq, len, 0, st),
+                                 seq, len, 0, true, st),
               "8-bit kv cache store");
     Q3VL_CUDA(launch_attention_q8(c, q, B, *kv8, seq, len, 1, true, o, ws + L8->att, st),
               "8-bit decode attention");
@@ -1266,7 +1266,7 @@ int q3vl_kv_store_q8(const q3vl_config* cfg, const void* k, const void* v, int64
     Q3VL_TRY(check_ptr(seq, "seq", false));
     Q3VL_TRY(check_ptr(len, "len", false));
     return cuda_check(launch_kv_store_q8(*cfg, k, v, ld, T, starts, B, *kv, seq, len, 0,
-                                         ST(stream)),
+                                         false, ST(stream)),
                       "8-bit kv cache store");
   });
 }

@@ -8,8 +8,8 @@
 // and once as V transposed (dims x tokens). What multiplies them has to be e4m3 too,
 // so q and the probabilities are split into a sum of e4m3 parts, each 2^-4 of
 // the one before:
-//   q = 2^e (a1 + a2 / 16 + a3 / 256), exact for most bf16 values, and to
-//       2^-18 of the head's largest element for all;
+//   q = 2^e (a1 + a2 / 16 + a3 / 256), exact down to 2^-18 of the head's largest
+//       element, and to 2^-26 of it below;
 //   p = a1 + a2 / 16, to 2^-8 of p (the two halves of a step at 2^-4 each),
 //       or 2^-22 of the largest.
 // The parts are further columns of the narrow N operand, whose width costs
@@ -22,11 +22,17 @@
 // The chunks (128 tokens) of all sequences form one list, cut into equal,
 // contiguous parts, so that uneven lengths balance; a part is worked on by nkv
 // neighbouring CTAs, one per KV head, which read the same rows of the cache at
-// about the same time (with the heads one after the other in the list, XXX).
+// about the same time (two sequences of 131072 and 115000: 91 us, and 124 with
+// the heads one after the other in the list).
 // A part covers segments of one or more sequences; a segment that is a whole
 // sequence is finished in place, another leaves (o, max, sum) in the
 // workspace, in one of its CTA's two slots, and a second kernel joins them in
-// order (and writes the rows of sequences without tokens).
+// order (and writes the rows of sequences without tokens). A single sequence is
+// balanced as it is: then the up to 16 parts of a head are one cluster, which
+// joins them over DSMEM and saves the second launch (2.4 us of the host's time;
+// on the device 512 tokens 6.1 us against 7.3, 4096 tokens 10.5 both). Inside a
+// decode call, whose next kernel's weights are on their way meanwhile, the
+// clusters gave nothing (66.5 us a layer against 64.8 at 128 tokens).
 //
 // Roles per CTA (224 threads, two CTAs per SM): warps 0-3 softmax (thread = token,
 // then dimension), warp 4 TMA, warp 5 MMA, warp 6 builds the q parts. Chunks go in
@@ -42,6 +48,7 @@ constexpr int kAqThreads = 224;
 constexpr int kAqTiles = 6;               // ring of 16 KB tiles, K and V in turn
 constexpr int kAqTile = 128 * 128;
 constexpr int kAqRec = 130;               // floats of a head's partial: o[128], max, sum
+constexpr int kAqMaxCluster = 16;
 
 template <int G>
 struct AqCfg {
@@ -71,7 +78,9 @@ struct AttnQ8Params {
   int plus;                 // tokens attended: len[b] + plus
   int early;                // all blocks but each sequence's last are final before the dependency
   int B, nkv;
+  int most;                 // chunks that a slot can hold
   int parts;                // of the chunk list; nkv CTAs each
+  int cluster;              // one sequence: the parts of a head are a cluster
   float scale_log2;         // log2(e) / sqrt(128)
   __nv_bfloat16* o;         // [B][nh*128]
   float* part;              // [parts][nkv][2][G][kAqRec]
@@ -151,13 +160,15 @@ struct AqIter {
   int u = 0, u1 = 0;
   AqBatch t{};
   __device__ AqIter(const AttnQ8Params& p_, const AqList& l) : p(p_), list(l) {
-    const int part = blockIdx.x / p.nkv, parts = aq_parts_of(p, l.total);
+    // a part's heads side by side, or in a cluster a head's parts
+    const int part = p.cluster ? blockIdx.x % p.parts : blockIdx.x / p.nkv;
+    const int parts = aq_parts_of(p, l.total);
     if (part < parts) {
       u = static_cast<int>(static_cast<uint32_t>(l.total * part) / static_cast<uint32_t>(parts));
       u1 = static_cast<int>(static_cast<uint32_t>(l.total * (part + 1)) /
                             static_cast<uint32_t>(parts));
     }
-    t.g = static_cast<int>(blockIdx.x % p.nkv);
+    t.g = static_cast<int>(p.cluster ? blockIdx.x / p.parts : blockIdx.x % p.nkv);
   }
   __device__ bool next(AqBatch& out) {
     if (t.c + t.nb < t.c1) {
@@ -258,8 +269,9 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   tc_fence_after();
 
   // lengths and slots are inputs of the call, not of the kernel before
-  if (!p.early || warp < 4 || warp == 6) griddep_wait();
+  if (!p.early) griddep_wait();
   const AqList list(p, lane, blockIdx.x == 0 && warp == 4);
+  if (p.early && (warp < 4 || warp == 6)) griddep_wait();
   if (warp == 4) {
     AqIter<kBat> ik(p, list), iv(p, list);
     AqBatch bk, bv;
@@ -432,6 +444,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     AqIter<kBat> it(p, list);
     AqBatch a;
     int j = 0;
+    float* rec = reinterpret_cast<float*>(s_tile);  // this CTA's record, once the ring is done
+    if (p.cluster && it.u >= it.u1) {  // no chunks: an empty record
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        rec[h * kAqRec + t] = 0.f;
+        if (t == 0) { rec[h * kAqRec + 128] = -INFINITY; rec[h * kAqRec + 129] = 0.f; }
+      }
+    }
     float m_run[G], l_run[G], o_run[G], fade[G];
     while (it.next(a)) {
       if (a.first()) {
@@ -553,9 +573,10 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
           if (lane == 0) s_wl[warp * 8 + h] = l;
         }
         softmax_sync();
-        const bool whole = a.c0 == 0 && a.c1 == a.nc;
+        const bool whole = !p.cluster && a.c0 == 0 && a.c1 == a.nc;
         __nv_bfloat16* ob = p.o + (int64_t(a.b) * p.nkv + a.g) * G * 128 + t;
-        float* pb = p.part + (int64_t(blockIdx.x) * 2 + (a.c0 == 0 ? 1 : 0)) * G * kAqRec;
+        float* pb = p.cluster ? rec
+                              : p.part + (int64_t(blockIdx.x) * 2 + (a.c0 == 0 ? 1 : 0)) * G * kAqRec;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float l = (s_wl[h] + s_wl[8 + h]) + (s_wl[16 + h] + s_wl[24 + h]);
@@ -576,6 +597,38 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
+  }
+  if (p.cluster) {
+    cluster_sync();  // every CTA's record is in its shared memory
+    if (t < 128) {
+      const int g = blockIdx.x / p.parts;
+      for (int i = static_cast<int>(cluster_ctarank()) * 128 + t; i < G * 128; i += p.parts * 128) {
+        const int h = i >> 7, d = i & 127;
+        const uint32_t own = smem_u32(s_tile) + h * kAqRec * 4;
+        // all records requested before any is used
+        float m[kAqMaxCluster], l[kAqMaxCluster], o[kAqMaxCluster], M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kAqMaxCluster; ++k) {
+          const uint32_t at = map_to_cta(own, static_cast<uint32_t>(k < p.parts ? k : 0));
+          m[k] = k < p.parts ? ld_dsmem_f32(at + 128 * 4) : -INFINITY;
+          l[k] = k < p.parts ? ld_dsmem_f32(at + 129 * 4) : 0.f;
+          o[k] = k < p.parts ? ld_dsmem_f32(at + 4 * d) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kAqMaxCluster; ++k) M = fmaxf(M, m[k]);
+        float num = 0.f, den = 0.f;
+#pragma unroll
+        for (int k = 0; k < kAqMaxCluster; ++k) {
+          if (l[k] == 0.f) continue;  // empty
+          const float w = ex2_approx(m[k] - M);
+          num = fmaf(w, o[k], num);
+          den = fmaf(w, l[k], den);
+        }
+        // no tokens at all: zeros
+        p.o[(int64_t(g) * G + h) * 128 + d] = __float2bfloat16_rn(den == 0.f ? 0.f : num / den);
+      }
+    }
+    cluster_sync();  // no record leaves while another CTA may read it
   }
 }
 
@@ -676,12 +729,36 @@ int aq_parts(int nkv, int B, int64_t cap) {
 }
 
 template <int G>
-cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnQ8Params& p,
+cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnQ8Params p,
                      cudaStream_t st) {
   auto kern = attn_q8_kernel<G>;
   cudaError_t e = smem_attr_at_least(reinterpret_cast<const void*>(kern), AqCfg<G>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_plain(kern, dim3(p.parts * p.nkv), dim3(kAqThreads), AqCfg<G>::kSmem, st, tmK, tmV, p);
+  if (p.B == 1 && !p.early) {
+    // the largest clusters of which all heads' are resident at once
+    const void* fn = reinterpret_cast<const void*>(kern);
+    e = allow_nonportable_clusters(fn);
+    if (e != cudaSuccess) return e;
+    int cs = p.most < kAqMaxCluster ? p.most : kAqMaxCluster;
+    for (; cs >= 2; --cs) {
+      int n = 0;
+      e = max_active_clusters(fn, kAqThreads, AqCfg<G>::kSmem, cs, &n);
+      if (e != cudaSuccess) return e;
+      if (n >= p.nkv) break;
+    }
+    if (3 * cs >= (p.most < p.parts ? p.most : p.parts)) {
+      p.cluster = 1;
+      p.parts = cs;
+      e = launch_pdl_cluster(kern, dim3(cs * p.nkv), dim3(kAqThreads), AqCfg<G>::kSmem, st, cs, tmK,
+                             tmV, p);
+      return e != cudaSuccess ? e : counted_launch(1);
+    }
+  }
+  e = launch_pdl_plain(kern, dim3(p.parts * p.nkv), dim3(kAqThreads), AqCfg<G>::kSmem, st, tmK, tmV,
+                       p);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl_plain(attn_q8_join_kernel, dim3(p.B * p.nkv * G), dim3(128), 0, st, p, G);
+  return e != cudaSuccess ? e : counted_launch(2);
 }
 
 }  // namespace
@@ -707,23 +784,19 @@ cudaError_t launch_attention_q8(const q3vl_config& c, const void* q, int B,
   p.seq = seq; p.len = len; p.plus = plus; p.early = early ? 1 : 0;
   p.B = B; p.nkv = c.n_kv_heads;
   p.parts = aq_parts(c.n_kv_heads, B, kv.cap);
+  p.most = p.nblk;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / 11.313708498984761);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.part = static_cast<float*>(ws);
   p.err = device_error_ptr();
   const int G = c.n_heads / c.n_kv_heads;
-  cudaError_t e = cudaErrorInvalidValue;
   switch (G) {
-    case 1: e = launch_g<1>(tmK, tmV, p, st); break;
-    case 2: e = launch_g<2>(tmK, tmV, p, st); break;
-    case 4: e = launch_g<4>(tmK, tmV, p, st); break;
-    case 8: e = launch_g<8>(tmK, tmV, p, st); break;
-    default: break;
+    case 1: return launch_g<1>(tmK, tmV, p, st);
+    case 2: return launch_g<2>(tmK, tmV, p, st);
+    case 4: return launch_g<4>(tmK, tmV, p, st);
+    case 8: return launch_g<8>(tmK, tmV, p, st);
+    default: return cudaErrorInvalidValue;
   }
-  if (e != cudaSuccess) return e;
-  e = launch_pdl_plain(attn_q8_join_kernel, dim3(B * c.n_heads), dim3(128), 0, st, p, G);
-  if (e != cudaSuccess) return e;
-  return counted_launch(2);
 }
 
 }  // namespace q3vl

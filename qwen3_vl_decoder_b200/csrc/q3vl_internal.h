@@ -214,10 +214,11 @@ cudaError_t launch_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, co
                              bool out_bf16, cudaStream_t st);
 // Rows of B sequences into the 8-bit cache. seq == nullptr: B = 1, all T rows
 // to rows 0.. of slot seq0. starts == nullptr with seq: one row per sequence.
+// `early`: starts, seq and len are final before the kernel in front of this one.
 cudaError_t launch_kv_store_q8(const q3vl_config& c, const void* k, const void* v, int64_t ld,
                                int64_t T, const int32_t* starts, int B,
                                const q3vl_kv_cache_q8& kv, const int32_t* seq, const int32_t* len,
-                               int32_t seq0, cudaStream_t st);
+                               int32_t seq0, bool early, cudaStream_t st);
 size_t attention_q8_ws_bytes(const q3vl_config& c, int B, int64_t cap);
 // `plus`: 1 = rows 0..len[b] (the new row was just appended), 0 = rows
 // 0..len[b]-1. `early`: the full blocks below len[b] were written before this
