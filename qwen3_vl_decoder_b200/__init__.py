@@ -58,6 +58,8 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream=None):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
     # the current device's current stream, without building a Stream object (3 us a call)
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
 

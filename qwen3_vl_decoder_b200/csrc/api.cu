@@ -1150,6 +1150,15 @@ int q3vl_add_rms_norm_q8(const q3vl_config* cfg, const void* x, const void* delt
     if (gain != nullptr) Q3VL_TRY(check_ptr(gain, "gain"));
     Q3VL_TRY(check_ptr(q, "q"));
     Q3VL_TRY(check_ptr(scales, "scales", false));
+    // rows are read ahead of those written
+    const size_t qb = size_t(S) * cfg->hidden, xb = qb * elem_bytes(*cfg);
+    Q3VL_TRY(check_gap_free(q, qb, x, xb, "q"));
+    if (delta != nullptr) {
+      Q3VL_TRY(check_gap_free(q, qb, delta, xb, "q"));
+      Q3VL_TRY(check_gap_free(q, qb, h, xb, "q"));
+      if (h != x) Q3VL_TRY(check_gap_free(h, xb, x, xb, "h (unless it is x)"));
+      if (h != delta) Q3VL_TRY(check_gap_free(h, xb, delta, xb, "h (unless it is delta)"));
+    }
     return cuda_check(launch_add_rms_norm_q8(*cfg, x, delta, S, gain, h, q, scales, ST(stream)),
                       "8-bit norm");
   });
@@ -1290,6 +1299,8 @@ int q3vl_attention_q8(const q3vl_config* cfg, const void* q, int32_t B,
     Q3VL_TRY(check_ptr(seq, "seq", false));
     Q3VL_TRY(check_ptr(len, "len", false));
     Q3VL_TRY(check_ptr(o, "o"));
+    const size_t ob = size_t(B) * q_dim(*cfg) * 2;
+    if (o != q) Q3VL_TRY(check_gap_free(o, ob, q, ob, "o (unless it is q)"));
     const size_t need = attention_q8_ws_bytes(*cfg, B, kv->cap);
     if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) != 0 || ws_bytes < need)
       return set_error(Q3VL_EWORKSPACE, "8-bit attention workspace too small: need " +
