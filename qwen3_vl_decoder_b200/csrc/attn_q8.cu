@@ -29,8 +29,9 @@
 // workspace, in one of its CTA's two slots, and a second kernel joins them in
 // order (and writes the rows of sequences without tokens). A single sequence is
 // balanced as it is: then the up to 16 parts of a head are one cluster, which
-// joins them over DSMEM and saves the second launch (2.4 us of the host's time;
-// on the device 512 tokens 6.1 us against 7.3, 4096 tokens 10.5 both). Inside a
+// joins them over DSMEM and saves the second launch (512 tokens 6.1 us against
+// 7.3, 4096 tokens 9.4 against 10.5, 32768 tokens 20.4 against 22.8; and 2.4 us
+// of the host's time). Inside a
 // decode call, whose next kernel's weights are on their way meanwhile, the
 // clusters gave nothing (66.5 us a layer against 64.8 at 128 tokens).
 //
@@ -735,18 +736,19 @@ cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnQ8Param
   cudaError_t e = smem_attr_at_least(reinterpret_cast<const void*>(kern), AqCfg<G>::kSmem);
   if (e != cudaSuccess) return e;
   if (p.B == 1 && !p.early) {
-    // the largest clusters of which all heads' are resident at once
+    // up to 16 parts of each head while two CTAs per SM hold them all, if that is
+    // not far fewer than the list would have
     const void* fn = reinterpret_cast<const void*>(kern);
-    e = allow_nonportable_clusters(fn);
-    if (e != cudaSuccess) return e;
-    int cs = p.most < kAqMaxCluster ? p.most : kAqMaxCluster;
-    for (; cs >= 2; --cs) {
-      int n = 0;
-      e = max_active_clusters(fn, kAqThreads, AqCfg<G>::kSmem, cs, &n);
+    int cs = 2 * sm_count() / p.nkv, n = 0;
+    if (cs > kAqMaxCluster) cs = kAqMaxCluster;
+    if (cs > p.most) cs = p.most;
+    if (cs >= 1 && 3 * cs >= (p.most < p.parts ? p.most : p.parts)) {
+      e = allow_nonportable_clusters(fn);
+      if (e == cudaSuccess)
+        e = max_active_clusters(fn, kAqThreads, AqCfg<G>::kSmem, cs, &n);
       if (e != cudaSuccess) return e;
-      if (n >= p.nkv) break;
     }
-    if (3 * cs >= (p.most < p.parts ? p.most : p.parts)) {
+    if (n >= 1) {
       p.cluster = 1;
       p.parts = cs;
       e = launch_pdl_cluster(kern, dim3(cs * p.nkv), dim3(kAqThreads), AqCfg<G>::kSmem, st, cs, tmK,
