@@ -381,7 +381,8 @@ int q3vl_lm_head(const q3vl_config* cfg, const void* x, int32_t B, const void* f
  * The pages describe no 8-bit form; these calls exist because decode is bound
  * by the bytes of the weights and of the cache. An 8-bit element is an OCP
  * e4m3 byte (4 exponent bits, 3 mantissa bits, no infinity); it stands for
- * e4m3 * 2^(u - 127), u being the E8M0 byte of its block. The scale of a
+ * e4m3 * 2^(u - 127), u being the E8M0 byte of its block (1 <= u <= 254: the
+ * calls write no other, and expect no other in a cache). The scale of a
  * block whose largest finite magnitude is A is the smallest power of two
  * 2^s, s >= -126, with A <= 448 * 2^s (2^-126 for A = 0); elements are
  * divided by it and rounded to nearest even. An element that is not finite is
