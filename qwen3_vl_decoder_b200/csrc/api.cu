@@ -448,7 +448,7 @@ int run_layer(const q3vl_config& c, const q3vl_layer& w, void* x, int64_t S, cha
   if (kv8 != nullptr) {
     const char* k = static_cast<const char*>(qkv) + q_dim(c) * 2;
     Q3VL_CUDA(launch_kv_store_q8(c, k, k + kv_dim(c) * 2, qkv_dim(c), S, nullptr, 1, *kv8, nullptr,
-                                 nullptr, kv_seq, false, st),
+                                 nullptr, kv_seq, st),
               "8-bit kv cache store");
   }
   stage_event(3, st);
@@ -639,10 +639,8 @@ int run_decode_layer(const q3vl_config& c, const q3vl_layer& w, void* x, int32_t
     a.seq = reinterpret_cast<const int32_t*>(ws + L8->iota);
     a.len = reinterpret_cast<const int32_t*>(ws + L8->zero);
     Q3VL_CUDA(launch_decode_gemm(Epi::kQkv, a, st), "decode qkv projection");
-    Q3VL_CUDA(launch_kv_store_q8(c, ws + L8->k_new, ws + L8->v_new, kv_dim(c), B, nullptr, B, *kv8,
-                                 seq, len, 0, true, st),
-              "8-bit kv cache store");
-    Q3VL_CUDA(launch_attention_q8(c, q, B, *kv8, seq, len, 1, true, o, ws + L8->att, st),
+    Q3VL_CUDA(launch_attention_q8(c, q, B, *kv8, seq, len, ws + L8->k_new, ws + L8->v_new, o,
+                                  ws + L8->att, st),
               "8-bit decode attention");
   }
   // P6 (+ the row sums of squares of h for P7)
@@ -1275,7 +1273,7 @@ int q3vl_kv_store_q8(const q3vl_config* cfg, const void* k, const void* v, int64
     Q3VL_TRY(check_ptr(seq, "seq", false));
     Q3VL_TRY(check_ptr(len, "len", false));
     return cuda_check(launch_kv_store_q8(*cfg, k, v, ld, T, starts, B, *kv, seq, len, 0,
-                                         false, ST(stream)),
+                                         ST(stream)),
                       "8-bit kv cache store");
   });
 }
@@ -1305,7 +1303,7 @@ int q3vl_attention_q8(const q3vl_config* cfg, const void* q, int32_t B,
     if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) != 0 || ws_bytes < need)
       return set_error(Q3VL_EWORKSPACE, "8-bit attention workspace too small: need " +
                                             std::to_string(need) + " bytes, 256-byte aligned");
-    return cuda_check(launch_attention_q8(*cfg, q, B, *kv, seq, len, 0, false, o, ws, ST(stream)),
+    return cuda_check(launch_attention_q8(*cfg, q, B, *kv, seq, len, nullptr, nullptr, o, ws, ST(stream)),
                       "8-bit attention");
   });
 }

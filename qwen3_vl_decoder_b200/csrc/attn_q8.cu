@@ -33,7 +33,13 @@
 // 7.3, 4096 tokens 9.4 against 10.5, 32768 tokens 20.4 against 22.8; and 2.4 us
 // of the host's time). Inside a
 // decode call, whose next kernel's weights are on their way meanwhile, the
-// clusters gave nothing (66.5 us a layer against 64.8 at 128 tokens).
+// clusters gave nothing.
+//
+// Inside a decode call the token's own row is appended here (k_new): the q warp
+// of the CTA that holds a sequence's last chunk stores it by the rule of
+// kv_store_q8_kernel, in front of that chunk's loads. (With a store kernel of
+// its own: 113.7 us a layer for 32 sequences of 4096 tokens, 110.8 so; 64 of
+// 8192 268 and 259.)
 //
 // Roles per CTA (224 threads, two CTAs per SM): warps 0-3 softmax (thread = token,
 // then dimension), warp 4 TMA, warp 5 MMA, warp 6 builds the q parts. Chunks go in
@@ -64,20 +70,25 @@ struct AqCfg {
   static_assert(cSfP + 4 <= kCols, "TMEM columns");
   static constexpr size_t kSmem = 1024 + size_t(kAqTiles) * kAqTile + size_t(kBat) * kP +
                                   2 * kQ + 2 * 512 + 2 * 4 * 8 * 4 + 4 * 8 * 4 +
-                                  (2 * kAqTiles + 9) * 8 + 64;
+                                  (2 * kAqTiles + 9) * 8 + 4 * 2 * 4 + 64;
   static_assert(kSmem <= 115712, "two CTAs per SM");
 };
 
 struct AttnQ8Params {
   const __nv_bfloat16* q;   // [B][nh*128]
-  const uint8_t* ks;        // scales [n_seq][nblk][nkv]
-  const uint8_t* vs;
+  uint8_t* kc;              // the cache [n_seq][cap][nkv*128] (written where rows are appended)
+  uint8_t* vc;
+  uint8_t* ks;              // scales [n_seq][nblk][nkv]
+  uint8_t* vs;
+  const __nv_bfloat16* k_new;  // [B][nkv*128]: this token's rows, to row len[b]; or null
+  const __nv_bfloat16* v_new;
   int64_t cap;
   int n_seq, nblk;
   const int32_t* seq;
   const int32_t* len;
   int plus;                 // tokens attended: len[b] + plus
-  int early;                // all blocks but each sequence's last are final before the dependency
+  int early;                // seq, len and all blocks but each sequence's last are final before the
+                            // dependency
   int B, nkv;
   int most;                 // chunks that a slot can hold
   int parts;                // of the chunk list; nkv CTAs each
@@ -202,7 +213,7 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t w) {
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
 
-template <int G>
+template <int G, bool APPEND>
 __global__ void __launch_bounds__(kAqThreads, 2)
 attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                AttnQ8Params p) {
@@ -224,7 +235,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   uint64_t* drain = o_full + 1;
   float* s_wm = reinterpret_cast<float*>(drain + 1);      // [2][4 warps][8] maxima
   float* s_wl = s_wm + 2 * 4 * 8;                          // [4 warps][8] sums
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_wl + 4 * 8);
+  uint32_t* s_sc = reinterpret_cast<uint32_t*>(s_wl + 4 * 8);  // [4][2] scales of appended-to blocks
+  uint32_t* tmem_slot = s_sc + 4 * 2;
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -270,21 +282,23 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   tc_fence_after();
 
   // lengths and slots are inputs of the call, not of the kernel before
-  if (!p.early) griddep_wait();
+  if (!APPEND) griddep_wait();
   const AqList list(p, lane, blockIdx.x == 0 && warp == 4);
-  if (p.early && (warp < 4 || warp == 6)) griddep_wait();
+  if (APPEND && (warp < 4 || warp == 6)) griddep_wait();
   if (warp == 4) {
     AqIter<kBat> ik(p, list), iv(p, list);
     AqBatch bk, bv;
-    int stage = 0, issued = 0;
+    int stage = 0, issued = 0, seg = -1;
     uint32_t ph = 1;
-    bool ok = true, waited = !p.early;
-    auto load = [&](const AqBatch& a, const CUtensorMap* tm) {
+    bool ok = true;
+    auto load = [&](const AqBatch& a, const CUtensorMap* tm, bool keys) {
+      if (keys && a.first()) ++seg;
       for (int i = 0; i < a.nb && ok; ++i) {
-        if (!waited && a.c + i == a.nc - 1) {  // the block with the newest row
-          griddep_wait();
-          waited = true;
-        }
+        // the block that the q warp appends to (V's tiles come behind K's)
+        if (APPEND && keys && a.c + i == a.nc - 1)
+          ok = __all_sync(0xffffffffu, mbar_wait(q_full + (seg & 1), (seg >> 1) & 1, p.err,
+                                                 kWhereAttnQ8, s_abort));
+        if (!ok) break;
         ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, ph, p.err, kWhereAttnQ8, s_abort));
         if (!ok) break;
         if (elect_one()) {
@@ -297,15 +311,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         if (++stage == kAqTiles) { stage = 0; ph ^= 1; }
       }
     };
-    if (ik.next(bk)) load(bk, &tmK);
+    if (ik.next(bk)) load(bk, &tmK, true);
     while (ok && iv.next(bv)) {
-      if (ik.next(bk)) load(bk, &tmK);
-      if (ok) load(bv, &tmV);
+      if (ik.next(bk)) load(bk, &tmK, true);
+      if (ok) load(bv, &tmV, false);
     }
     // every issued load lands before the CTA may exit
     for (int i = issued > kAqTiles ? issued - kAqTiles : 0; i < issued; ++i)
       mbar_wait(full + i % kAqTiles, (i / kAqTiles) & 1, p.err, kWhereAttnQ8, nullptr);
-    if (!waited) griddep_wait();
   } else if (warp == 5) {
     constexpr uint32_t id_s = idesc_mxf8(128, NS), id_o = idesc_mxf8(128, 16) | (1u << 15);
     AqIter<kBat> is(p, list), iv(p, list);
@@ -397,6 +410,45 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     AqIter<kBat> it(p, list);
     AqBatch a;
     int seg = 0;
+    // this token's K and V rows into row len - 1 of the sequence, 4 elements a
+    // lane; the scales of their blocks to sc
+    auto append = [&](const AqBatch& e, uint32_t* sc) {
+      const int row = e.len - 1, blk = row >> 7;
+      const int64_t si = (int64_t(e.slot) * p.nblk + blk) * p.nkv + e.g, rs = int64_t(p.nkv) * 128;
+      const int64_t ni = (int64_t(e.b) * p.nkv + e.g) * 128 + 4 * lane;
+      const bool keeps = (row & 127) != 0;  // the block holds earlier rows
+      if (!dcheck(e.slot < p.n_seq && row < p.cap, p.err, kWhereDbgQ8)) return;
+      const uint2 now[2] = {*reinterpret_cast<const uint2*>(p.k_new + ni),
+                            *reinterpret_cast<const uint2*>(p.v_new + ni)};
+      const uint32_t old[2] = {keeps ? p.ks[si] : 0u, keeps ? p.vs[si] : 0u};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = unpack_bf16x2(now[i].x), y = unpack_bf16x2(now[i].y);
+        uint32_t u = e8m0_of_amax(redux_max(fmaxf(fmaxf(finite_abs(x.x), finite_abs(x.y)),
+                                                  fmaxf(finite_abs(y.x), finite_abs(y.y)))));
+        const uint32_t was = old[i];
+        if (keeps && was >= u) u = was;
+        uint8_t* dst = (i == 0 ? p.kc : p.vc) + int64_t(e.slot) * p.cap * rs + e.g * 128 + 4 * lane;
+        if (keeps && u > was) {
+          const float m = u - was > 126 ? 0.f : e8m0_inverse(127 + (u - was));
+#pragma unroll 4
+          for (int r = blk * 128; r < row; ++r) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(dst + r * rs);
+            const float4 f = unpack_e4m3x4(*w);
+            *w = pack_e4m3x4(f.x * m, f.y * m, f.z * m, f.w * m);
+          }
+        }
+        const float s = e8m0_inverse(u);
+        *reinterpret_cast<uint32_t*>(dst + row * rs) = pack_e4m3x4(x.x * s, x.y * s, y.x * s, y.y * s);
+        if (lane == 0) {
+          (i == 0 ? p.ks : p.vs)[si] = static_cast<uint8_t>(u);
+          sc[i] = u;
+        }
+      }
+      // the tile's loads go through the async proxy
+      __threadfence();
+      asm volatile("fence.proxy.async;" ::: "memory");
+    };
     while (it.next(a)) {
       if (!a.first()) continue;
       const int qb = seg & 1;
@@ -408,6 +460,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       uint2 raw[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) raw[h] = *reinterpret_cast<const uint2*>(src + h * 128);
+      if (APPEND && a.c1 == a.nc) append(a, s_sc + 2 * (seg & 3));
       uint32_t word = kNoScale;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -444,7 +497,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // all four pass the same named barriers.
     AqIter<kBat> it(p, list);
     AqBatch a;
-    int j = 0;
+    int j = 0, seg = -1;
     float* rec = reinterpret_cast<float*>(s_tile);  // this CTA's record, once the ring is done
     if (p.cluster && it.u >= it.u1) {  // no chunks: an empty record
 #pragma unroll
@@ -456,6 +509,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     float m_run[G], l_run[G], o_run[G], fade[G];
     while (it.next(a)) {
       if (a.first()) {
+        ++seg;
 #pragma unroll
         for (int h = 0; h < G; ++h) { m_run[h] = -INFINITY; l_run[h] = o_run[h] = fade[h] = 0.f; }
       }
@@ -465,12 +519,23 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < kBat; ++i) {
         const int64_t at = si + int64_t(min(i, a.nb - 1)) * p.nkv;
-        kb[i] = p.ks[at];
-        vb[i] = p.vs[at];
+        const bool appended = APPEND && a.c + i >= a.nc - 1;
+        kb[i] = appended ? 127 : p.ks[at];
+        vb[i] = appended ? 127 : p.vs[at];
       }
       mbar_wait(s_full + (j & 1), (j >> 1) & 1, p.err, kWhereAttnQ8, s_abort);
       __syncwarp();
       tc_fence_after();
+      // the q warp left them before the q parts of these scores; it comes back
+      // to the slot four segments on, behind products of two segments on, which
+      // wait for this batch
+      if (APPEND)
+#pragma unroll
+        for (int i = 0; i < kBat; ++i)
+          if (a.c + i == a.nc - 1) {
+            kb[i] = static_cast<uint8_t>(s_sc[2 * (seg & 3)]);
+            vb[i] = static_cast<uint8_t>(s_sc[2 * (seg & 3) + 1]);
+          }
       float sc[kBat][G];
 #pragma unroll
       for (int i = 0; i < kBat; ++i) {
@@ -755,10 +820,10 @@ int aq_parts(int nkv, int B, int64_t cap) {
 template <int G>
 cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnQ8Params p,
                      cudaStream_t st) {
-  auto kern = attn_q8_kernel<G>;
+  auto kern = p.k_new != nullptr ? attn_q8_kernel<G, true> : attn_q8_kernel<G, false>;
   cudaError_t e = smem_attr_at_least(reinterpret_cast<const void*>(kern), AqCfg<G>::kSmem);
   if (e != cudaSuccess) return e;
-  if (p.B == 1 && !p.early) {
+  if (p.B == 1 && p.k_new == nullptr) {
     // up to 16 parts of each head while two CTAs per SM hold them all, if that is
     // not far fewer than the list would have
     const void* fn = reinterpret_cast<const void*>(kern);
@@ -797,8 +862,8 @@ size_t attention_q8_ws_bytes(const q3vl_config& c, int B, int64_t cap) {
 
 cudaError_t launch_attention_q8(const q3vl_config& c, const void* q, int B,
                                 const q3vl_kv_cache_q8& kv, const int32_t* seq,
-                                const int32_t* len, int plus, bool early, void* o, void* ws,
-                                cudaStream_t st) {
+                                const int32_t* len, const void* k_new, const void* v_new, void* o,
+                                void* ws, cudaStream_t st) {
   const uint64_t rows = uint64_t(kv.n_seq) * uint64_t(kv.cap), dkv = uint64_t(kv_dim(c));
   CUtensorMap tmK, tmV;
   if (!make_tmap_u8(&tmK, kv.k, rows, dkv, dkv, 128, 128) ||
@@ -806,9 +871,12 @@ cudaError_t launch_attention_q8(const q3vl_config& c, const void* q, int B,
     return cudaErrorInvalidValue;
   AttnQ8Params p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
-  p.ks = kv.k_scale; p.vs = kv.v_scale;
+  p.kc = kv.k; p.vc = kv.v; p.ks = kv.k_scale; p.vs = kv.v_scale;
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
   p.cap = kv.cap; p.n_seq = kv.n_seq; p.nblk = static_cast<int>((kv.cap + 127) / 128);
-  p.seq = seq; p.len = len; p.plus = plus; p.early = early ? 1 : 0;
+  p.seq = seq; p.len = len;
+  p.plus = p.early = k_new != nullptr ? 1 : 0;
   p.B = B; p.nkv = c.n_kv_heads;
   p.parts = aq_parts(c.n_kv_heads, B, kv.cap);
   p.most = p.nblk;

@@ -214,19 +214,20 @@ cudaError_t launch_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, co
                              bool out_bf16, cudaStream_t st);
 // Rows of B sequences into the 8-bit cache. seq == nullptr: B = 1, all T rows
 // to rows 0.. of slot seq0. starts == nullptr with seq: one row per sequence.
-// `early`: starts, seq and len are final before the kernel in front of this one.
 cudaError_t launch_kv_store_q8(const q3vl_config& c, const void* k, const void* v, int64_t ld,
                                int64_t T, const int32_t* starts, int B,
                                const q3vl_kv_cache_q8& kv, const int32_t* seq, const int32_t* len,
-                               int32_t seq0, bool early, cudaStream_t st);
+                               int32_t seq0, cudaStream_t st);
 size_t attention_q8_ws_bytes(const q3vl_config& c, int B, int64_t cap);
-// `plus`: 1 = rows 0..len[b] (the new row was just appended), 0 = rows
-// 0..len[b]-1. `early`: the full blocks below len[b] were written before this
-// call's first kernel, so they may be read before the kernel's own dependency.
+// Rows 0..len[b]-1, or, with k_new and v_new ([B][nkv*hd] bf16, this token's
+// rows): appends them as row len[b] by launch_kv_store_q8's rule and attends to
+// rows 0..len[b]. Then seq, len and the full blocks below len[b] have to be
+// final before the call's first kernel: they are read before this kernel's own
+// dependency.
 cudaError_t launch_attention_q8(const q3vl_config& c, const void* q, int B,
                                 const q3vl_kv_cache_q8& kv, const int32_t* seq,
-                                const int32_t* len, int plus, bool early, void* o, void* ws,
-                                cudaStream_t st);
+                                const int32_t* len, const void* k_new, const void* v_new, void* o,
+                                void* ws, cudaStream_t st);
 // Indexes of a one-row-per-sequence scratch "cache": iota[b] = b, zero[b] = 0.
 cudaError_t launch_iota_zero(int B, int32_t* iota, int32_t* zero, cudaStream_t st);
 

@@ -227,7 +227,6 @@ struct StoreQ8Params {
   uint8_t* vs;
   int64_t cap;
   int n_seq, nkv;
-  int early;              // starts, seq and len are final before the dependency
   int32_t* err;
 };
 
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(256, 4) kv_store_q8_kernel(StoreQ8Params p) {
   __shared__ float s_a[8];
   if (t == 0) s_item[0] = -1;
   griddep_launch_dependents();
-  if (!p.early) griddep_wait();
+  griddep_wait();
   __syncthreads();
   // Starts that decrease would let two sequences claim one place: then nothing
   // is stored. B <= 256: one sequence per thread.
@@ -266,9 +265,7 @@ __global__ void __launch_bounds__(256, 4) kv_store_q8_kernel(StoreQ8Params p) {
       s_blk = len / 128 + static_cast<int>(j);
     }
   }
-  falls = __syncthreads_or(falls ? 1 : 0) != 0;
-  if (p.early) griddep_wait();
-  if (falls) return;
+  if (__syncthreads_or(falls ? 1 : 0)) return;
   const int slot = s_item[0];
   if (slot < 0) return;
   const int len = s_item[1], n = s_item[3], blk = s_blk;
@@ -404,9 +401,8 @@ cudaError_t launch_quantize_weight_q8(const q3vl_config& c, const void* w, int64
 cudaError_t launch_kv_store_q8(const q3vl_config& c, const void* k, const void* v, int64_t ld,
                                int64_t T, const int32_t* starts, int B,
                                const q3vl_kv_cache_q8& kv, const int32_t* seq, const int32_t* len,
-                               int32_t seq0, bool early, cudaStream_t st) {
+                               int32_t seq0, cudaStream_t st) {
   StoreQ8Params p{};
-  p.early = early ? 1 : 0;
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);
   p.ld = ld; p.T = T; p.starts = starts; p.B = B; p.seq = seq; p.len = len; p.seq0 = seq0;

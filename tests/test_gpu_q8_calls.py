@@ -9,8 +9,9 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_common import host, q3
+from gpu_common import host, layer_on_device, q3
 from oracle import q8_oracle as Q
+import q3vl_synth as syn
 from test_gpu_q8 import (HD, _cache, _cfg, _check_attention, _check_linear, _e8, _fill, _gen,
                          _rows8, _weight)
 
@@ -256,6 +257,48 @@ def test_captured_calls_replayed_with_other_data():
     m.check_device()
 
 
+@pytest.mark.parametrize("level", [2.0 ** -9, 1.0, 300.0], ids=["grows", "even", "keeps"])
+@pytest.mark.parametrize("lens", [[0, 1, 127, 128, 129, 255, 256, 700], [300], [7] * 70],
+                         ids=["borders", "one", "b70"])
+def test_decode_appends_the_row_that_the_store_would(lens, level):
+    # the same layer step on a bf16 cache tells the row; the 8-bit cache gets it by the store's
+    # rule: below, near and above the magnitude of what its blocks hold
+    m = q3()
+    w = syn.Q2B_LAYER
+    cfg = m.config_of(w)
+    _, packed = layer_on_device(w)
+    B, nkv, cap = len(lens), w.n_kv_heads, max(lens) + 1
+    kv8, kv = m.kv_caches(cfg, 1, B, cap, dtype="fp8")[0], m.kv_caches(cfg, 1, B, cap)[0]
+    seq, ln = _i32(*reversed(range(B))), _i32(*lens)
+    ref = []
+    for b, n in enumerate(lens):
+        rows = (level * torch.randn(2, max(n, 1), nkv * HD, generator=_gen(200 + b))).to(
+            torch.bfloat16)
+        slot = []
+        for i in range(2):
+            c, s = np.zeros((cap, nkv, HD)), np.ones((-(-cap // 128), nkv))
+            if n:
+                Q.store(c, s, rows[i, :n].double().numpy().reshape(n, nkv, HD), 0)
+            slot.append((c, s))
+        if n:
+            r = rows.cuda()
+            m.kv_store_q8(cfg, r[0], r[1], kv8, seq[b:b + 1].clone(), _i32(0), _i32(0, n))
+        ref.append(slot)
+    x = torch.randn(B, w.hidden, generator=_gen(300)).to(torch.bfloat16).cuda()
+    pos = ln.repeat(3, 1).contiguous()
+    m.layer_decode(cfg, packed, x.clone(), pos, kv, seq, ln)      # writes the bf16 rows alone
+    m.layer_decode(cfg, packed, x.clone(), pos, kv8, seq, ln)
+    m.check_device()
+    for b, n in enumerate(lens):
+        at = B - 1 - b
+        for i, (t, sc, full) in enumerate(((kv8.k, kv8.k_scale, kv.k), (kv8.v, kv8.v_scale, kv.v))):
+            c, s = ref[b][i]
+            Q.store(c, s, host(full[at, n:n + 1]).reshape(1, nkv, HD), n)
+            assert np.array_equal(host(t[at, :n + 1]).reshape(n + 1, nkv, HD), c[:n + 1]), (b, i)
+            nb = n // 128 + 1
+            assert np.array_equal(_e8(sc[at, :nb]), s[:nb]), (b, i)
+
+
 DEBUG = r"""
 import sys
 sys.path[:0] = [{root!r}, {tests!r}]
@@ -270,6 +313,7 @@ for lens, new, cap in T.STORE:
     T.test_store_is_exact(lens, new, cap, 300.0)
 for nh, nkv, lens in T.ATTEND[:4]:
     T.test_attention_matches_the_oracle(nh, nkv, lens)
+T.test_layer_decode_over_the_8bit_cache(T.syn.Q2B_LAYER, [0, 1, 127, 128, 300])
 T.test_norm_matches_the_oracle(700, 2560, "bf16", True, True)
 m.check_device()
 print("clean")
