@@ -210,7 +210,10 @@ quantize_weight_kernel(const T* __restrict__ w, int64_t N, int64_t K, uint8_t* _
 // the rounding. The items of sequence b sit at floor(starts[b] / 128) + 2 b
 // along grid x: n rows touch at most floor(n / 128) + 2 blocks, so the items
 // of two sequences never meet and no scan is needed; a place that no item
-// takes exits. Bound by memory: 3 bytes per element.
+// takes exits. Bound by memory, 3 bytes per element, and by instructions: the
+// maximum is taken on pairs of bf16 as they were loaded and infinities are left
+// to a branch (15000 rows of 8 heads, K and V, 19.0 us or 4.9 TB/s; 22.2 with
+// the finite magnitudes picked out one by one).
 // ---------------------------------------------------------------------------
 struct StoreQ8Params {
   const __nv_bfloat16* k;
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(256, 4) kv_store_q8_kernel(StoreQ8Params p) {
   const int t = threadIdx.x, lane = t & 31;
   __shared__ int s_item[4];  // slot (-1: none), rows cached, first source row, rows
   __shared__ int s_blk;
-  __shared__ float s_a[8];
+  __shared__ float s_a[2][8];
   if (t == 0) s_item[0] = -1;
   griddep_launch_dependents();
   griddep_wait();
@@ -283,25 +286,39 @@ __global__ void __launch_bounds__(256, 4) kv_store_q8_kernel(StoreQ8Params p) {
     f[i].zero();
     if (lo + r < hi && dcheck(s0 + r < p.T, p.err, kWhereDbgQ8)) f[i].load(src + (s0 + r) * p.ld);
   }
-  // the magnitudes of two bf16 to a word compare as integers; 0x7f80 and above
-  // are not finite
-  uint32_t top = 0;
+  // The largest magnitude, two elements to a word; NaN drops out. An infinity
+  // is rare enough for a second look at the block, that leaves it out.
+  auto block_max = [&](float v, int set) {
+    v = warp_max(v);
+    if (lane == 0) s_a[set][t >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v = fmaxf(v, s_a[set][i]);
+    return v;
+  };
+  __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t w[4] = {f[i].v[0].x, f[i].v[0].y, f[i].v[0].z, f[i].v[0].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t m = w[j] & 0x7fff7fffu;
-      top = __vmaxu2(top, m & __vcmpltu2(m, 0x7f807f80u));
-    }
+    for (int j = 0; j < 4; ++j)
+      top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
   }
-  float a = warp_max(fmaxf(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u)));
-  if (lane == 0) s_a[t >> 5] = a;
   const bool keeps = blk * 128 < len;  // the block holds earlier rows
   const uint32_t was = keeps ? *scale : 0u;
-  __syncthreads();
+  float a = block_max(fmaxf(__low2float(top), __high2float(top)), 0);
+  const bool infinite = a == INFINITY;
+  if (infinite) {
+    a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, s_a[i]);
+    for (int i = 0; i < 8; ++i) {
+      float v[8];
+      f[i].floats(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a = fmaxf(a, finite_abs(v[j]));
+    }
+    a = block_max(a, 1);
+  }
   uint32_t e = e8m0_of_amax(a);
   if (keeps && was >= e) e = was;
   if (t == 0) *scale = static_cast<uint8_t>(e);
@@ -320,15 +337,23 @@ __global__ void __launch_bounds__(256, 4) kv_store_q8_kernel(StoreQ8Params p) {
     }
   }
   const float s = e8m0_inverse(e);
+  const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = lo + (t >> 4) + 16 * i;
     if (r < hi && dcheck(r < p.cap, p.err, kWhereDbgQ8)) {
+      uint64_t x[4];
       float v[8];
-      f[i].floats(v);
+      f[i].pairs(x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f2_unpack(f2_mul(x[j], s2), v[2 * j], v[2 * j + 1]);
+      if (infinite) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], 0.f, v[j]);
+      }
       uint2 w;
-      w.x = pack_e4m3x4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
-      w.y = pack_e4m3x4(v[4] * s, v[5] * s, v[6] * s, v[7] * s);
+      w.x = pack_e4m3x4_finite(v[0], v[1], v[2], v[3]);
+      w.y = pack_e4m3x4_finite(v[4], v[5], v[6], v[7]);
       *reinterpret_cast<uint2*>(dst + int64_t(r) * rs) = w;
     }
   }
