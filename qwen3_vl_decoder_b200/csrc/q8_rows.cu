@@ -21,6 +21,13 @@ struct Raw8 {
   __device__ __forceinline__ void floats(float (&f)[8]) const {
     load8(reinterpret_cast<const T*>(v), f);
   }
+  // bf16 only: += o, rounded to bf16
+  __device__ __forceinline__ void add(const Raw8& o) {
+    __nv_bfloat162* a = reinterpret_cast<__nv_bfloat162*>(v);
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(o.v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = __hadd2(a[j], b[j]);
+  }
   // the same as four pairs for the packed arithmetic
   __device__ __forceinline__ void pairs(uint64_t (&f)[4]) const {
     float s[8];
@@ -39,9 +46,11 @@ struct Raw8 {
 // 7 bytes per bf16 element with a delta (3 without). Rows up to 8192 wide (NV =
 // 1) go through as many blocks as fit, which request the next row before they
 // reduce this one; that wants 48 registers, for three quarters of the threads.
-// Measured, against a block per row without: bf16 with a delta 4096 x 2560 16.2
-// us (18.2), 8192 x 5120 58 (75, 5.1 TB/s); fp32 2129 x 5120 14.4 (19.3). Rows on
-// their way in a ring of bulk copies instead of registers: 18.9 us at the first.
+// Instructions come close behind memory, hence the packed arithmetic and the
+// branches for what only infinities need. Measured: bf16 with a delta
+// 4096 x 2560 14.7 us, 8192 x 5120 52 (5.7 TB/s), fp32 2129 x 5120 14.2; a block
+// per row without look-ahead 18.2, 75, 19.3, and at the first rows on their way
+// in a ring of bulk copies instead of registers 18.9.
 // ---------------------------------------------------------------------------
 template <typename T, int NV, bool PRE, bool DELTA>
 __global__ void __maxnreg__(NV == 1 ? 48 : 64)
@@ -75,8 +84,15 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
     for (int i = 0; i < NV; ++i) {
       const int u = t + i * blockDim.x;
       if (!PRE) request(row, u);
+      if constexpr (DELTA && sizeof(T) == 2) {
+        // A sum of two bf16 that is inexact in fp32 has one of them below 2^-16
+        // of the other, and rounds to that other either way: so a packed bf16
+        // addition gives the bits of the fp32 sum rounded to bf16.
+        xn.add(dn);
+        if (u < units) *reinterpret_cast<uint4*>(h + row * width + 8 * u) = xn.v[0];
+      }
       xn.pairs(f[i]);
-      if (DELTA) {
+      if constexpr (DELTA && sizeof(T) == 4) {
         uint64_t d[4];
         dn.pairs(d);
         float v[8];
@@ -115,15 +131,25 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
       if (gain != nullptr) {
         uint64_t g[4];
         gn.pairs(g);
+        if (sizeof(T) == 2 && inv == 0.f) {  // the sum overflowed: zeros, whatever the gain
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[i][j] = f2_mul(f[i][j], 0);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // f * inv * g rounded once: about one value in a million lies so
           // near a border of e4m3 that an error in the last place turns it
-          // over (rounding f * inv as well is 1.3 us faster at 4096 x 2560 and
-          // turns over two to three times as many)
-          const uint64_t y = f2_mul(f[i][j], inv2);
-          const uint64_t rest = f2_fma(f[i][j], lo2, f2_fma(f[i][j], inv2, f2_mul(f[i][j], minus2)));
-          f[i][j] = f2_fma(y, g[j], f2_mul(rest, g[j]));
+          // over, and rounding f * inv as well turns over two to three times
+          // as many. A product of two bf16 is exact.
+          if constexpr (sizeof(T) == 2) {
+            const uint64_t fg = f2_mul(f[i][j], g[j]);
+            f[i][j] = f2_fma(fg, inv2, f2_mul(fg, lo2));
+          } else {
+            const uint64_t y = f2_mul(f[i][j], inv2);
+            const uint64_t rest =
+                f2_fma(f[i][j], lo2, f2_fma(f[i][j], inv2, f2_mul(f[i][j], minus2)));
+            f[i][j] = f2_fma(y, g[j], f2_mul(rest, g[j]));
+          }
         }
       }
       float v[8], a = 0.f;
