@@ -529,7 +529,7 @@ def _add_rms_norm_q8(cfg, x, gain, delta, h, st):
     if h is None:
         h = torch.empty_like(x)
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-    sc = x.new_empty((S, -(-H // Q8_BLOCK)), dtype=torch.float8_e8m0fnu)
+    sc = x.new_empty(S, -(-H // Q8_BLOCK), dtype=torch.float8_e8m0fnu)
     rc = lib().q3vl_add_rms_norm_q8(
         ctypes.byref(cfg), x.data_ptr(), None if delta is None else delta.data_ptr(), S,
         None if gain is None else gain.data_ptr(), h.data_ptr(), q.data_ptr(), sc.data_ptr(), st)
@@ -566,7 +566,7 @@ def linear_q8(xq: torch.Tensor, scales: torch.Tensor, lin: LinearQ8,
 
 def _linear_q8(xq, scales, lin, resid, out_dtype, out, M, N, K, st):
     if out is None:
-        out = xq.new_empty((M, N), dtype=out_dtype)
+        out = xq.new_empty(M, N, dtype=out_dtype)
     rc = lib().q3vl_linear_q8(
         xq.data_ptr(), scales.data_ptr(), M, lin.weight.data_ptr(), lin.scales.data_ptr(), N, K,
         None if resid is None else resid.data_ptr(), out.data_ptr(),
