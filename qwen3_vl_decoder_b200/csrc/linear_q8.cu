@@ -700,10 +700,12 @@ SkSched sk_sched(int64_t M, int64_t N, int64_t K) {
   const int gpcs = sm_count() / 18 > 1 ? sm_count() / 18 : 1;
   while (splits > 1 && (32 / splits) * gpcs < work) --splits;
   s.splits = static_cast<int>(splits < 1 ? 1 : splits);
-  // a ring as deep as the CTAs that share an SM allow, no deeper than the work
-  const size_t ring = size_t(work * s.splits > sm_count() ? 108 : 200) * 1024;
+  // a ring that leaves room for a second CTA on the SM, this kernel's or the
+  // next one's, no deeper than the work (200 KB where there is one CTA per SM
+  // kept the next launch out: 14.5 us against 8.5 in a row of 1 x 9728 x 2560,
+  // split seven ways so)
   const int most = (kblk + s.splits - 1) / s.splits;
-  int st = static_cast<int>(ring / stage);
+  int st = static_cast<int>(size_t(108 * 1024) / stage);
   st = st < 2 ? 2 : (st > 8 ? 8 : st);
   s.stages = st > most ? (most < 2 ? 2 : most) : st;
   s.smem = 1024 + size_t(s.stages) * stage + size_t(4) * kScaleBytes +
