@@ -403,7 +403,7 @@ int q3vl_lm_head(const q3vl_config* cfg, const void* x, int32_t B, const void* f
  *           NULL (it may then be NULL).
  * q:        device e4m3 [S, H] out, 16-byte aligned.
  * scales:   device E8M0 [S, ceil(H / 128)] out.
- * H <= 32768. */
+ * q and h overlap no input otherwise. H <= 32768. */
 int q3vl_add_rms_norm_q8(const q3vl_config* cfg, const void* x, const void* delta, int64_t S,
                          const void* gain, void* h, uint8_t* q, uint8_t* scales,
                          q3vl_stream stream);
@@ -479,7 +479,7 @@ size_t q3vl_attention_q8_workspace_bytes(const q3vl_config* cfg, int32_t B, int6
  * seq: device int32 [B], slots in [0, n_seq); several rows may share one.
  * len: device int32 [B], 0 <= len[b] <= cap. A slot or length out of range is
  *      the device error Q3VL_ERANGE and gives a zero row.
- * o:   device bf16 [B, nh*hd] out, 16-byte aligned.
+ * o:   device bf16 [B, nh*hd] out, 16-byte aligned; may be q.
  * ws:  >= q3vl_attention_q8_workspace_bytes bytes, 256-byte aligned.
  * 1 <= B <= 256, n_heads / n_kv_heads in {1, 2, 4, 8}. */
 int q3vl_attention_q8(const q3vl_config* cfg, const void* q, int32_t B,

@@ -257,7 +257,6 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
   }
-  griddep_launch_dependents();
   if (warp < 4) {
     // p parts of the columns from 2 G on stay zero
     for (int i = t; i < kBat * C::kP / 16; i += 128)
@@ -270,6 +269,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();  // behind the allocation: no later grid's can come before it
   const uint32_t lf = static_cast<uint32_t>((warp & 3) * 32) << 16;
   if (warp < 4) {
     // constant scales: ones for K and for the first p parts, 2^-4 for the second
