@@ -121,12 +121,22 @@ __device__ __forceinline__ int aq_parts_of(const AttnQ8Params& p, int total) {
   return min(p.parts, total);
 }
 
+// A part's heads are neighbouring CTAs (grid [parts][nkv]); in cluster mode a
+// head's parts are (grid [nkv][parts]).
+__device__ __forceinline__ int aq_part(const AttnQ8Params& p) {
+  return static_cast<int>(p.cluster ? blockIdx.x : blockIdx.y);
+}
+__device__ __forceinline__ int aq_head(const AttnQ8Params& p) {
+  return static_cast<int>(p.cluster ? blockIdx.y : blockIdx.x);
+}
+
 // Chunks of the sequences of one lane, 8 l .. 8 l + 7, and how many come before
 // them. Every role's warp makes its own: no barrier stands between the lengths
 // and the first load.
 struct AqList {
   uint32_t n[4];            // two counts (<= 1024) to a word
   int base, total;
+  int u0, u1;               // this CTA's part of the list
   __device__ AqList(const AttnQ8Params& p, int lane, bool report) {
     int sum = 0;
 #pragma unroll
@@ -146,6 +156,12 @@ struct AqList {
     }
     base = inc - sum;
     total = __shfl_sync(0xffffffffu, inc, 31);
+    const int part = aq_part(p), parts = aq_parts_of(p, total);
+    u0 = u1 = 0;
+    if (part < parts) {
+      u0 = static_cast<int>(static_cast<uint32_t>(total * part) / static_cast<uint32_t>(parts));
+      u1 = static_cast<int>(static_cast<uint32_t>(total * (part + 1)) / static_cast<uint32_t>(parts));
+    }
   }
   // The sequence that chunk u of the list belongs to (whole warp).
   __device__ void find(int u, int& b, int& start, int& nc) const {
@@ -169,18 +185,10 @@ template <int kBat>
 struct AqIter {
   const AttnQ8Params& p;
   const AqList& list;
-  int u = 0, u1 = 0;
+  int u, u1;
   AqBatch t{};
-  __device__ AqIter(const AttnQ8Params& p_, const AqList& l) : p(p_), list(l) {
-    // a part's heads side by side, or in a cluster a head's parts
-    const int part = p.cluster ? blockIdx.x % p.parts : blockIdx.x / p.nkv;
-    const int parts = aq_parts_of(p, l.total);
-    if (part < parts) {
-      u = static_cast<int>(static_cast<uint32_t>(l.total * part) / static_cast<uint32_t>(parts));
-      u1 = static_cast<int>(static_cast<uint32_t>(l.total * (part + 1)) /
-                            static_cast<uint32_t>(parts));
-    }
-    t.g = static_cast<int>(p.cluster ? blockIdx.x / p.parts : blockIdx.x % p.nkv);
+  __device__ AqIter(const AttnQ8Params& p_, const AqList& l) : p(p_), list(l), u(l.u0), u1(l.u1) {
+    t.g = aq_head(p);
   }
   __device__ bool next(AqBatch& out) {
     if (t.c + t.nb < t.c1) {
@@ -283,7 +291,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
   // lengths and slots are inputs of the call, not of the kernel before
   if (!APPEND) griddep_wait();
-  const AqList list(p, lane, blockIdx.x == 0 && warp == 4);
+  const AqList list(p, lane, blockIdx.x == 0 && blockIdx.y == 0 && warp == 4);
   if (APPEND && (warp < 4 || warp == 6)) griddep_wait();
   if (warp == 4) {
     AqIter<kBat> ik(p, list), iv(p, list);
@@ -642,7 +650,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         const bool whole = !p.cluster && a.c0 == 0 && a.c1 == a.nc;
         __nv_bfloat16* ob = p.o + (int64_t(a.b) * p.nkv + a.g) * G * 128 + t;
         float* pb = p.cluster ? rec
-                              : p.part + (int64_t(blockIdx.x) * 2 + (a.c0 == 0 ? 1 : 0)) * G * kAqRec;
+                              : p.part + ((int64_t(blockIdx.y) * p.nkv + a.g) * 2 + (a.c0 == 0 ? 1 : 0)) * G *
+                                             kAqRec;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float l = (s_wl[h] + s_wl[8 + h]) + (s_wl[16 + h] + s_wl[24 + h]);
@@ -667,7 +676,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   if (p.cluster) {
     cluster_sync();  // every CTA's record is in its shared memory
     if (t < 128) {
-      const int g = blockIdx.x / p.parts;
+      const int g = blockIdx.y;
       for (int i = static_cast<int>(cluster_ctarank()) * 128 + t; i < G * 128; i += p.parts * 128) {
         const int h = i >> 7, d = i & 127;
         const uint32_t own = smem_u32(s_tile) + h * kAqRec * 4;
@@ -839,12 +848,12 @@ cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, AttnQ8Param
     if (n >= 1) {
       p.cluster = 1;
       p.parts = cs;
-      e = launch_pdl_cluster(kern, dim3(cs * p.nkv), dim3(kAqThreads), AqCfg<G>::kSmem, st, cs, tmK,
+      e = launch_pdl_cluster(kern, dim3(cs, p.nkv), dim3(kAqThreads), AqCfg<G>::kSmem, st, cs, tmK,
                              tmV, p);
       return e != cudaSuccess ? e : counted_launch(1);
     }
   }
-  e = launch_pdl_plain(kern, dim3(p.parts * p.nkv), dim3(kAqThreads), AqCfg<G>::kSmem, st, tmK, tmV,
+  e = launch_pdl_plain(kern, dim3(p.nkv, p.parts), dim3(kAqThreads), AqCfg<G>::kSmem, st, tmK, tmV,
                        p);
   if (e != cudaSuccess) return e;
   const dim3 rows(p.B * p.nkv * G);
