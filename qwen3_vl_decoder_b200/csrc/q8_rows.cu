@@ -37,6 +37,43 @@ struct Raw8 {
   }
 };
 
+// 1 / sqrt(ss / width + eps) in two parts, ss the sum of the lanes' values (one
+// warp). The last two levels of the sum, the quotient and the root keep their
+// remainders: what is left is an error of a tenth of a unit in the last place.
+__device__ __forceinline__ float2 inv_rms(float ss, float width, float eps) {
+#pragma unroll
+  for (int o = 16; o > 2; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  float lo = 0.f;
+#pragma unroll
+  for (int o = 2; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, ss, o), yl = __shfl_xor_sync(0xffffffffu, lo, o);
+    const float z = ss + y, b = z - ss;
+    lo = (lo + yl) + ((ss - (z - b)) + (y - b));
+    ss = z;
+  }
+  const float q = ss / width;
+  const float ql = (fmaf(-q, width, ss) + lo) / width;
+  const float var = q + eps, b = var - q;
+  const float vl = ql + ((q - (var - b)) + (eps - b));
+  const float inv = 1.0f / sqrtf(var);
+  // (var + vl) inv^2 = 1 - d, so 1 / sqrt(var + vl) = inv (1 + d / 2)
+  const float a = var * inv, al = fmaf(var, inv, -a);
+  float il = 0.5f * inv * (fmaf(-a, inv, 1.f) - (al + vl * inv) * inv);
+  if (!(fabsf(il) < inv)) il = 0.f;  // var 0 or not finite
+  return make_float2(inv, il);
+}
+
+// v = h / rms * gain / scale was rounded onto the middle of two e4m3 steps:
+// the neighbour on the side on which it lay (one value in a million; below
+// 2^-6, where e4m3 has fewer bits, a middle keeps its rounding).
+__device__ __noinline__ float off_middle(float v, float h, float gain, float inv, float inv_lo,
+                                         float s) {
+  const double y = fabs(double(h) * double(gain) * (double(inv) + double(inv_lo)) * double(s));
+  const double m = fabs(double(v));
+  const uint32_t bits = __float_as_uint(v);
+  return __uint_as_float(y > m ? bits + 1 : y < m ? bits - 1 : bits);
+}
+
 // ---------------------------------------------------------------------------
 // h = x + delta; y = h * (1 / rms(h)) * gain; e4m3 of y, a scale per 128
 // columns. A block takes rows blockIdx.x, + gridDim.x, ...; a thread takes
@@ -47,10 +84,12 @@ struct Raw8 {
 // 1) go through as many blocks as fit, which request the next row before they
 // reduce this one; that wants 48 registers, for three quarters of the threads.
 // Instructions come close behind memory, hence the packed arithmetic and the
-// branches for what only infinities need. Measured: bf16 with a delta
-// 4096 x 2560 14.7 us, 8192 x 5120 52 (5.7 TB/s), fp32 2129 x 5120 14.2; a block
-// per row without look-ahead 18.2, 75, 19.3, and at the first rows on their way
-// in a ring of bulk copies instead of registers 18.9.
+// branches for what only infinities need. One warp makes 1 / rms for the block.
+// Measured: bf16 with a delta 4096 x 2560 15.0 us, 8192 x 5120 55 (5.4 TB/s),
+// fp32 2129 x 5120 15.7; with an fp32 1 / rms made by every warp, which turned
+// about one e4m3 value in 10 million over, 14.7, 52, 14.4. Before that step a
+// block per row without look-ahead took 18.2, 75, 19.3, and a ring of bulk
+// copies instead of registers 18.9 at the first size.
 // ---------------------------------------------------------------------------
 template <typename T, int NV, bool PRE, bool DELTA>
 __global__ void __maxnreg__(NV == 1 ? 48 : 64)
@@ -59,6 +98,7 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
   const int t = threadIdx.x, lane = t & 31;
   const int units = width / 8;
   __shared__ float s_ss[2][32];
+  __shared__ float2 s_inv[2];
   griddep_launch_dependents();
   griddep_wait();
   Raw8<T> xn, dn, gn;
@@ -113,14 +153,14 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
       ss = warp_sum(ss + ss1);
       if (lane == 0) s_ss[par][t >> 5] = ss;
       __syncthreads();
-      ss = lane < (blockDim.x >> 5) ? s_ss[par][lane] : 0.f;
-      ss = warp_sum(ss);
-      const float var = ss / static_cast<float>(width) + eps;
-      inv = 1.0f / sqrtf(var);
-      // var inv^2 = 1 - d, so 1 / sqrt(var) = inv (1 + d / 2)
-      const float a = var * inv, b = fmaf(var, inv, -a);
-      inv_lo = 0.5f * inv * (fmaf(-a, inv, 1.f) - b * inv);
-      if (!(fabsf(inv_lo) < inv)) inv_lo = 0.f;  // var 0 or not finite
+      if (t < 32) {
+        const float2 r = inv_rms(lane < (blockDim.x >> 5) ? s_ss[par][lane] : 0.f,
+                                 static_cast<float>(width), eps);
+        if (lane == 0) s_inv[par] = r;
+      }
+      __syncthreads();
+      inv = s_inv[par].x;
+      inv_lo = s_inv[par].y;
     }
     const uint64_t inv2 = f2_pack(inv, inv), minus2 = f2_pack(-inv, -inv),
                    lo2 = f2_pack(inv_lo, inv_lo);
@@ -139,8 +179,8 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
         for (int j = 0; j < 4; ++j) {
           // f * inv * g rounded once: about one value in a million lies so
           // near a border of e4m3 that an error in the last place turns it
-          // over, and rounding f * inv as well turns over two to three times
-          // as many. A product of two bf16 is exact.
+          // over, and rounding f * inv as well turned over two to three times
+          // as many. What lands on a border all the same goes to off_middle. A product of two bf16 is exact.
           if constexpr (sizeof(T) == 2) {
             const uint64_t fg = f2_mul(f[i][j], g[j]);
             f[i][j] = f2_fma(fg, inv2, f2_mul(fg, lo2));
@@ -174,6 +214,21 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
       if (infinite) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], 0.f, v[j]);
+      }
+      if (gain != nullptr) {
+        // low 20 bits 0x80000: rounded onto the middle of two steps
+        uint32_t low = ~0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          low = min(low, __float_as_uint(v[j]) * 4096u + 0x80000000u);
+        if (low == 0 && u < units) {
+          const T* hr = (DELTA ? h : x) + row * width + 8 * u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if ((__float_as_uint(v[j]) & 0xfffffu) == 0x80000u)
+              v[j] = off_middle(v[j], static_cast<float>(hr[j]),
+                                static_cast<float>(gain[8 * u + j]), inv, inv_lo, s);
+        }
       }
       if (u < units) {
         uint2 w;
