@@ -546,6 +546,8 @@ def linear_q8(xq: torch.Tensor, scales: torch.Tensor, lin: LinearQ8,
     if not (isinstance(xq, torch.Tensor) and xq.dtype is torch.float8_e4m3fn and
             xq.is_contiguous()):
         _arg(xq, "xq", (torch.float8_e4m3fn,))
+    if not isinstance(lin, LinearQ8):
+        raise Q3VLError(_abi.EINVAL, "lin must be a LinearQ8")
     N, K = lin.weight.shape
     shape, index = xq.shape, xq.get_device()
     if len(shape) != 2 or shape[1] != K:
@@ -587,6 +589,8 @@ def _lm_head_q8(cfg, x_rows, final_norm, lin, logits, ws, stream):
         raise Q3VLError(_abi.EINVAL, f"the weight is on {lin.weight.device}, x_rows on {x_rows.device}")
     if logits is not None:
         _arg(logits, "logits", (torch.float32,), (B, vocab), x_rows.device)
+    if ws is not None:
+        _arg(ws, "ws", (torch.uint8,), None, x_rows.device)
 
     def call(logits, ws, st):
         if logits is None:
@@ -617,6 +621,8 @@ def kv_store_q8(cfg: Config, k: torch.Tensor, v: torch.Tensor, kv: KvCacheQ8, se
     ranges of a QKV buffer. seq (distinct slots) and lens: int32 [B]; starts: int32 [B+1]. lens
     is not advanced.
     """
+    if not isinstance(kv, KvCacheQ8):
+        raise Q3VLError(_abi.EINVAL, "kv must be a KvCacheQ8")
     dkv, index = cfg.n_kv_heads * cfg.head_dim, kv._index
     shape, strides = k.shape, k.stride()
     T, B = shape[0], seq.numel()
@@ -670,6 +676,8 @@ def attention_q8(cfg: Config, q: torch.Tensor, kv: KvCacheQ8, seq: torch.Tensor,
                  ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """o [B, nh*128] bf16: the attention of query row b (q [B, nh*128] bf16) over rows
     0..lens[b]-1 of slot seq[b] of an 8-bit cache; a length of 0 gives a zero row."""
+    if not isinstance(kv, KvCacheQ8):
+        raise Q3VLError(_abi.EINVAL, "kv must be a KvCacheQ8")
     dq, dkv = cfg.n_heads * cfg.head_dim, cfg.n_kv_heads * cfg.head_dim
     if not (isinstance(q, torch.Tensor) and q.dtype is torch.bfloat16 and q.is_contiguous()):
         _arg(q, "q", (torch.bfloat16,))
@@ -685,6 +693,8 @@ def attention_q8(cfg: Config, q: torch.Tensor, kv: KvCacheQ8, seq: torch.Tensor,
     _ints(lens, "lens", B, kv)
     if o is not None and not _is(o, torch.bfloat16, shape, index):
         _arg(o, "o", (torch.bfloat16,), (B, dq), q.device)
+    if ws is not None:
+        _arg(ws, "ws", (torch.uint8,), None, q.device)
     return _run(q, index, stream, _attention_q8, cfg, q, B, kv, seq, lens, o, ws)
 
 

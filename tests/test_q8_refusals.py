@@ -1,6 +1,9 @@
 """Overlapping buffers of the 8-bit calls are refused before any CUDA call (no GPU)."""
 import ctypes
 
+import pytest
+import torch
+
 from test_abi import _cfg, lib  # noqa: F401  (fixture)
 
 
@@ -34,3 +37,27 @@ def test_attention_refuses_an_output_that_starts_inside_its_query(lib):  # noqa:
     assert att(q - 16) == -1 and b"overlap" in lib.q3vl_last_error()
     # apart or the same: the next check answers (the workspace)
     assert att(q) == -5 and att(q + 2 * width * B) == -5
+
+
+def test_binding_refuses_other_kinds_of_weights_caches_and_workspaces(lib):  # noqa: F811
+    import qwen3_vl_decoder_b200 as q3
+    c = _cfg()
+    i = torch.zeros(2, dtype=torch.int32)
+    k = torch.zeros(2, 1024, dtype=torch.bfloat16)
+    q = torch.zeros(2, 4096, dtype=torch.bfloat16)
+    w = torch.zeros(256, 2560, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    lin = q3.LinearQ8(w, torch.zeros(2, 20, dtype=torch.uint8).view(torch.float8_e8m0fnu))
+    scales = torch.zeros(2, 20, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+    kv, kv8 = (q3.kv_caches(c, 1, 2, 200, "cpu", dtype=d)[0] for d in ("bf16", "fp8"))
+    far = torch.empty(1 << 20, dtype=torch.uint8, device="meta")   # not the operands' device
+    wide = torch.empty(1 << 20, dtype=torch.float32)
+    for call, what in ((lambda: q3.linear_q8(w[:2], scales, w), "LinearQ8"),
+                       (lambda: q3.kv_store_q8(c, k, k, kv, i, i), "KvCacheQ8"),
+                       (lambda: q3.attention_q8(c, q, kv, i, i), "KvCacheQ8"),
+                       (lambda: q3.attention_q8(c, q, kv8, i, i, ws=far), "ws is on"),
+                       (lambda: q3.attention_q8(c, q, kv8, i, i, ws=wide), "ws must be"),
+                       (lambda: q3.lm_head(c, k.new_zeros(2, 2560), None, lin, ws=far), "ws is on"),
+                       (lambda: q3.lm_head(c, k.new_zeros(2, 2560), None, lin, ws=wide),
+                        "ws must be")):
+        with pytest.raises(q3.Q3VLError, match=what):
+            call()
