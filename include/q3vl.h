@@ -475,6 +475,10 @@ size_t q3vl_attention_q8_workspace_bytes(const q3vl_config* cfg, int32_t B, int6
 /* Attention of one query row per sequence over the 8-bit cache: query head h
  * of row b over rows 0 .. len[b] - 1 of KV head h / (nh/nkv) in slot seq[b],
  * scale 1/sqrt(hd). len[b] = 0 gives a zero row.
+ * Scores, maxima and sums are fp32. A probability is held to 2^-9 of itself,
+ * down to 2^-28 of the largest among the up to 64 rows that share its scale
+ * (32 of a block of 128, and the same 32 of the next block), below that to
+ * 2^-37 of that largest one.
  * q:   device bf16 [B, nh*hd], 16-byte aligned (after the norm and MRoPE).
  * seq: device int32 [B], slots in [0, n_seq); several rows may share one.
  * len: device int32 [B], 0 <= len[b] <= cap. A slot or length out of range is

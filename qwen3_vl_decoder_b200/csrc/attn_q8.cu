@@ -5,19 +5,27 @@
 // G = nh / nkv query heads that share it. The cache rows go from TMA to the
 // tensor core as they are stored, with no conversion: an e4m3 tile of 128
 // tokens is the MMA's M operand (kind::mxf8f6f4), once as K (tokens x dims)
-// and once as V transposed (dims x tokens). What multiplies them has to be e4m3 too,
-// so q and the probabilities are split into a sum of e4m3 parts, each 2^-4 of
-// the one before:
-//   q = 2^e (a1 + a2 / 16 + a3 / 256), exact down to 2^-18 of the head's largest
-//       element, and to 2^-26 of it below;
-//   p = a1 + a2 / 16, to 2^-8 of p (the two halves of a step at 2^-4 each),
-//       or 2^-22 of the largest.
+// and once as V transposed (dims x tokens). What multiplies them has 8 bits too,
+// so q and the probabilities are split into a sum of 8-bit parts:
+//   q = 2^e (a1 + a2 / 16 + a3 / 256), e4m3, exact down to 2^-18 of the head's
+//       largest element, and to 2^-26 of it below;
+//   p = 2^e (a1 + a2 / 8 + a3 / 64), e5m2, to 2^-9 of p (a rounding of 2^-3 in
+//       each part), as bf16 would hold it, down to 2^-28 of the largest p that
+//       shares the scale; what is smaller, to 2^-37 of that largest.
+// Tokens share p's scale 2^e where they share an E8M0 byte of the MMA, 32 tokens
+// of a chunk (and the same 32 places of the batch's other chunk): one softmax
+// warp, whose maximum is at hand. So the range does not depend on what other
+// tokens have: behind a first token of e^16 times the others' probability and a
+// small value row, thousands of tiny ones carry the output. (Two e4m3 parts
+// under one scale for all tokens, 2^-22 of the largest, lost up to all of it;
+// they took 8.7 us at 4096 tokens, 8.9 now, 60 at 131072, 62 now, and the same 56 for
+// 32 sequences of 4096.)
 // The parts are further columns of the narrow N operand, whose width costs
 // nothing: an MMA of 128 x N x 32 takes as long as its 4 KB of M operand do.
-// The factors 2^e, 2^-4i and the scale of the V block are E8M0 scales that the
-// tensor core applies; the scale of the K block goes into the softmax's.
+// The factors 2^e, 2^-4i, 2^-3i and the scale of the V block are E8M0 scales
+// that the tensor core applies; the scale of the K block goes into the softmax's.
 //
-//   S^T [128 tokens x 3G] = K [128 x 128] . Q^T       O^T [128 dims x 2G] = V^T . P^T
+//   S^T [128 tokens x 3G] = K [128 x 128] . Q^T       O^T [128 dims x 3G] = V^T . P^T
 //
 // The chunks (128 tokens) of all sequences form one list, cut into equal,
 // contiguous parts, so that uneven lengths balance; a part is worked on by nkv
@@ -59,12 +67,14 @@ constexpr int kAqMaxCluster = 16;
 
 template <int G>
 struct AqCfg {
-  static constexpr int NS = G == 8 ? 32 : 16;      // S columns: 3 G parts
+  static constexpr int NS = G == 8 ? 32 : 16;      // columns of S and O: 3 G parts
   static constexpr int kBat = 2;                   // chunks per batch
   static constexpr int kQ = NS * 128;              // q parts, e4m3
-  static constexpr int kP = 16 * 128;              // p parts of a chunk
+  // p parts of a chunk, e5m2. G = 8 keeps 24 of its 32 rows: the MMA reads the
+  // bytes behind them (the next chunk's, or q's) into columns that no one does.
+  static constexpr int kP = (G == 8 ? 24 : 16) * 128;
   // TMEM columns: S of two batches, O, scales of K (ones), q (two segments), V, p
-  static constexpr int cS = 0, cO = 2 * kBat * NS, cSfK = cO + 16, cSfQ = cSfK + 4,
+  static constexpr int cS = 0, cO = 2 * kBat * NS, cSfK = cO + NS, cSfQ = cSfK + 4,
                        cSfV = cSfQ + 8, cSfP = cSfV + 4;
   static constexpr uint32_t kCols = G == 8 ? 256 : 128;
   static_assert(cSfP + 4 <= kCols, "TMEM columns");
@@ -219,10 +229,19 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t w) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr), "r"(w)
                : "memory");
 }
+// e for probabilities 2^(s - M) of scores up to `top` <= M: the largest lies in
+// [2^e, 2^(e + 1)). At least -96, far below what fp32 sums keep and above the
+// end of the E8M0 bytes; also where there is no score (top = -inf) or M is NaN.
+__device__ __forceinline__ float aq_p_exponent(float top, float M) {
+  return fmaxf(floorf(top - M), -96.f);
+}
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
 
+// Registers: two CTAs per SM, and for up to four heads enough left beside them
+// for two blocks of the joining kernel, which then starts before this one ends
+// (4 sequences of 4096 tokens 14.5 us, and 16.9 with 118 registers).
 template <int G, bool APPEND>
-__global__ void __launch_bounds__(kAqThreads, 2)
+__global__ void __maxnreg__(G == 8 ? 128 : 112)
 attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                AttnQ8Params p) {
   using C = AqCfg<G>;
@@ -266,7 +285,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tmem_relinquish();
   }
   if (warp < 4) {
-    // p parts of the columns from 2 G on stay zero
+    // p parts of the columns from 3 G on stay zero
     for (int i = t; i < kBat * C::kP / 16; i += 128)
       *reinterpret_cast<uint4*>(s_p + 16 * i) = make_uint4(0, 0, 0, 0);
   } else if (warp == 6) {
@@ -280,9 +299,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   griddep_launch_dependents();  // behind the allocation: no later grid's can come before it
   const uint32_t lf = static_cast<uint32_t>((warp & 3) * 32) << 16;
   if (warp < 4) {
-    // constant scales: ones for K and for the first p parts, 2^-4 for the second
-    tmem_st4(tmem + lf + C::cSfK, kNoScale);
-    tmem_st4(tmem + lf + C::cSfP, lane < G ? kNoScale : 0x7b7b7b7bu);
+    tmem_st4(tmem + lf + C::cSfK, kNoScale);  // constant scales: ones for K
     tmem_st_wait();
   }
   tc_fence_before();
@@ -328,7 +345,8 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     for (int i = issued > kAqTiles ? issued - kAqTiles : 0; i < issued; ++i)
       mbar_wait(full + i % kAqTiles, (i / kAqTiles) & 1, p.err, kWhereAttnQ8, nullptr);
   } else if (warp == 5) {
-    constexpr uint32_t id_s = idesc_mxf8(128, NS), id_o = idesc_mxf8(128, 16) | (1u << 15);
+    constexpr uint32_t id_s = idesc_mxf8(128, NS);
+    constexpr uint32_t id_o = idesc_mxf8(128, NS) | (1u << 10) | (1u << 15);  // p e5m2, V transposed
     AqIter<kBat> is(p, list), iv(p, list);
     AqBatch bs, bv;
     int stage = 0, js = 0, jv = 0, seg = 0;
@@ -397,9 +415,10 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         const uint32_t id = id_o | (static_cast<uint32_t>(i) << 29);  // V's scale: byte i
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_mxf8_ss(tmem + C::cO, dv + 256 * kk, dp + 2 * kk, id, tmem + C::cSfV,
-                         tmem + C::cSfP, (i | kk) > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk)  // p's scale: byte kk
+            umma_mxf8_ss(tmem + C::cO, dv + 256 * kk, dp + 2 * kk,
+                         id | (static_cast<uint32_t>(kk) << 4), tmem + C::cSfV, tmem + C::cSfP,
+                         (i | kk) > 0 ? 1u : 0u);
           umma_commit(empty + stage);
           if (i == bv.nb - 1) umma_commit(o_full);
         }
@@ -515,9 +534,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       }
     }
     float m_run[G], l_run[G], o_run[G], fade[G];
+    // this lane's word of p's scales: row `lane` of the N operand is part
+    // lane / G of head lane % G; m_lane is that head's running maximum
+    const int row_part = lane / G, row_head = lane % G;
+    float m_lane = -INFINITY;
     while (it.next(a)) {
       if (a.first()) {
         ++seg;
+        m_lane = -INFINITY;
 #pragma unroll
         for (int h = 0; h < G; ++h) { m_run[h] = -INFINITY; l_run[h] = o_run[h] = fade[h] = 0.f; }
       }
@@ -579,26 +603,38 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                               m_run[h]);
         next_fade[h] = ex2_approx(m_run[h] - M);
         m_run[h] = M;
+        // 2^(e + 14) holds this warp's largest p, so p is 2^e times at most 2^15.
+        // The sums carry a factor 2^8, which the quotient drops.
+        const float e = aq_p_exponent(wm[warp * 8 + h], M);
         float l = 0.f;
 #pragma unroll
         for (int i = 0; i < kBat; ++i) {
-          // 2^8 p: the sums carry the factor as well, and the quotient drops it
-          sc[i][h] = ex2_approx(sc[i][h] - M + 8.f);
+          sc[i][h] = ex2_approx((sc[i][h] - M) + (14.f - e));
           l += sc[i][h];
         }
-        l_run[h] = l_run[h] * next_fade[h] + l;
+        l_run[h] = fmaf(l, __uint_as_float(static_cast<uint32_t>(int(e) + 127 + 8 - 14) << 23),
+                        l_run[h] * next_fade[h]);
       }
+      m_lane = fmaxf(fmaxf(fmaxf(wm[row_head], wm[8 + row_head]),
+                           fmaxf(wm[16 + row_head], wm[24 + row_head])), m_lane);
+      uint32_t pw = 0;  // byte w: the scale of the tokens of warp w
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        pw |= static_cast<uint32_t>(int(aq_p_exponent(wm[8 * w + row_head], m_lane)) + 127 + 8 -
+                                    14 - 3 * row_part) << (8 * w);
       // the batch before: its products, behind which P and V's scales are free
       auto fold = [&](int of) {
         mbar_wait(o_full, of & 1, p.err, kWhereAttnQ8, s_abort);
         __syncwarp();
         tc_fence_after();
-        uint32_t u[16];
-        tmem_ld16(tmem + lf + C::cO, u);
+        uint32_t u[NS];
+        if constexpr (NS == 16) tmem_ld16(tmem + lf + C::cO, u);
+        else tmem_ld32(tmem + lf + C::cO, u);
         tmem_ld_wait();
 #pragma unroll
         for (int h = 0; h < G; ++h)
-          o_run[h] = o_run[h] * fade[h] + (__uint_as_float(u[h]) + __uint_as_float(u[G + h]));
+          o_run[h] = o_run[h] * fade[h] + ((__uint_as_float(u[h]) + __uint_as_float(u[G + h])) +
+                                           __uint_as_float(u[2 * G + h]));
       };
       if (!a.first()) fold(j - 1);
 #pragma unroll
@@ -607,6 +643,7 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < kBat; ++i) vw |= uint32_t(vb[i]) << (8 * i);
       tmem_st4(tmem + lf + C::cSfV, vw);
+      tmem_st4(tmem + lf + C::cSfP, row_part < 3 ? pw : kNoScale);
 #pragma unroll
       for (int i = 0; i < kBat; ++i) {
         if (i >= a.nb) break;
@@ -615,14 +652,14 @@ attn_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
         for (int h = 0; h < (G + 3) / 4 * 4; ++h) v[h] = h < G ? sc[i][h < G ? h : 0] : 0.f;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
           for (int h0 = 0; h0 < G; h0 += 4) {
-            const uint32_t w = pack_e4m3x4(v[h0], v[h0 + 1], v[h0 + 2], v[h0 + 3]);
-            if (part == 0) {
-              const float4 r = unpack_e4m3x4(w);
-              v[h0] = (v[h0] - r.x) * 16.f; v[h0 + 1] = (v[h0 + 1] - r.y) * 16.f;
-              v[h0 + 2] = (v[h0 + 2] - r.z) * 16.f; v[h0 + 3] = (v[h0 + 3] - r.w) * 16.f;
+            const uint32_t w = pack_e5m2x4(v[h0], v[h0 + 1], v[h0 + 2], v[h0 + 3]);
+            if (part < 2) {
+              const float4 r = unpack_e5m2x4(w);
+              v[h0] = (v[h0] - r.x) * 8.f; v[h0 + 1] = (v[h0 + 1] - r.y) * 8.f;
+              v[h0 + 2] = (v[h0 + 2] - r.z) * 8.f; v[h0 + 3] = (v[h0 + 3] - r.w) * 8.f;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)

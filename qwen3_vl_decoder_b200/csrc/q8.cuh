@@ -60,6 +60,23 @@ __device__ __forceinline__ float4 unpack_e4m3x4(uint32_t w) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// The same for e5m2 (4 mantissa steps a factor of two, from 2^-16 to 57344),
+// for values of at most 57344 or NaN.
+__device__ __forceinline__ uint32_t pack_e5m2x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+__device__ __forceinline__ float4 unpack_e5m2x4(uint32_t w) {
+  uint32_t l, h;
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(l) : "h"(static_cast<uint16_t>(w & 0xffffu)));
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w >> 16)));
+  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&l));
+  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&h));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -102,12 +119,12 @@ __device__ __forceinline__ void store8(float* p, float (&f)[8]) {
 }
 
 // ---------------------------------------------------------------------------
-// tcgen05 with block scales (kind::mxf8f6f4: e4m3 operands, one E8M0 scale per
-// row and 32 columns, fp32 accumulation)
+// tcgen05 with block scales (kind::mxf8f6f4: e4m3 or e5m2 operands, one E8M0
+// scale per row and 32 columns, fp32 accumulation)
 // ---------------------------------------------------------------------------
 // Instruction descriptor: bits [4,6) and [29,31) choose the byte of B's and
 // A's scale words (idesc_sf adds them), [7,10) / [10,13) A / B format
-// (0 = e4m3), [17,23) N >> 3, 23 scale type (1 = E8M0), [24,29) M >> 4.
+// (0 = e4m3, 1 = e5m2), [17,23) N >> 3, 23 scale type (1 = E8M0), [24,29) M >> 4.
 __host__ __device__ constexpr uint32_t idesc_sf(uint32_t byte) { return (byte << 4) | (byte << 29); }
 __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
   return (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24);
