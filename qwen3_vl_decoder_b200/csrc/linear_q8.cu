@@ -125,12 +125,13 @@ __device__ __forceinline__ void finish4(const LinQ8Params& p, int64_t m, int64_t
 // Scale bytes k .. k + 3 of a row of `end` bytes as one word (the last byte
 // repeated behind the end). `words`: rows are whole, aligned words, as for
 // every K that is a multiple of 512; else four loads, which cost the warp that
-// makes the words four times the load instructions.
+// makes the words four times the load instructions. Coherent loads: the kernel
+// may be resident while the one before it writes these bytes.
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int k, int end, bool words) {
-  if (words && k + kSG <= end) return __ldg(reinterpret_cast<const uint32_t*>(row + k));
+  if (words && k + kSG <= end) return *reinterpret_cast<const uint32_t*>(row + k);
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < kSG; ++i) w |= uint32_t(__ldg(row + min(k + i, end - 1))) << (8 * i);
+  for (int i = 0; i < kSG; ++i) w |= uint32_t(row[min(k + i, end - 1)]) << (8 * i);
   return w;
 }
 
