@@ -314,60 +314,55 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
   // x][128], in its own (drained) stage ring; after a cluster barrier CTA
   // `split` finishes rows j = split (mod splits). Every thread of every CTA of
   // the cluster passes the same cluster barriers.
+  static_assert(kSkMaxNB <= 128, "a tile has to fit in the ring");
+  // S >= 2 stages of 128 (128 + NB) bytes hold NB rows of 512: NB <= 128
   __syncthreads();  // all roles done: loads landed, MMAs committed or abandoned
   const bool run = *abort_flag == 0;
   tc_fence_after();
   float* red = reinterpret_cast<float*>(smem);
-  const size_t ring = size_t(S) * (kABytes + b_bytes);
   const int rows = static_cast<int>(p.M - m0 < sc.NB ? p.M - m0 : sc.NB);
-  int chunk = static_cast<int>(ring / 512) / 16 * 16;  // rows per round
-  if (chunk > sc.NB) chunk = sc.NB;
+  if (warp >= 2 && run) {
+    const int q = warp & 3;
+    const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
 #pragma unroll 1
-  for (int j0 = 0; j0 < rows; j0 += chunk) {
-    const int nj = rows - j0 < chunk ? rows - j0 : chunk;
-    if (warp >= 2 && run) {
-      const int q = warp & 3;
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-#pragma unroll 1
-      for (int c0 = 0; c0 < nj; c0 += 16) {
-        uint32_t u[16];
-        tmem_ld16(tb + j0 + c0, u);
-        tmem_ld_wait();
+    for (int c0 = 0; c0 < rows; c0 += 16) {
+      uint32_t u[16];
+      tmem_ld16(tb + c0, u);
+      tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c0 + c < nj) red[(c0 + c) * 128 + 32 * q + lane] = __uint_as_float(u[c]);
-      }
+      for (int c = 0; c < 16; ++c)
+        if (c0 + c < rows) red[(c0 + c) * 128 + 32 * q + lane] = __uint_as_float(u[c]);
     }
-    cluster_sync();  // every CTA's partials of this round are in its shared memory
-    if (warp >= 2 && run) {
-#pragma unroll 1
-      for (int jj = split + (warp - 2) * sc.splits; jj < nj; jj += 8 * sc.splits) {
-        // two rows at a time, every split's values requested before any is
-        // added: one DSMEM round trip, then the sum in split order
-        const int j1 = jj + 4 * sc.splits;
-        float4 w[2][kSkMaxSplits];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t own = smem_u32(red + (i == 0 || j1 >= nj ? jj : j1) * 128 + 4 * lane);
-#pragma unroll
-          for (int sp = 0; sp < kSkMaxSplits; ++sp)
-            if (sp < sc.splits) w[i][sp] = ld_dsmem_f32x4(map_to_cta(own, sp));
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int sp = 0; sp < kSkMaxSplits; ++sp)
-            if (sp < sc.splits) {
-              v[0] += w[i][sp].x; v[1] += w[i][sp].y; v[2] += w[i][sp].z; v[3] += w[i][sp].w;
-            }
-          const int j = i == 0 ? jj : j1;
-          if (j < nj) finish4<T>(p, m0 + j0 + j, int64_t(tile) * 128 + 4 * lane, v);
-        }
-      }
-    }
-    cluster_sync();  // no CTA overwrites or leaves its buffer while another may read it
   }
+  cluster_sync();  // every CTA's partials are in its shared memory
+  if (warp >= 2 && run) {
+#pragma unroll 1
+    for (int jj = split + (warp - 2) * sc.splits; jj < rows; jj += 8 * sc.splits) {
+      // two rows at a time, every split's values requested before any is
+      // added: one DSMEM round trip, then the sum in split order
+      const int j1 = jj + 4 * sc.splits;
+      float4 w[2][kSkMaxSplits];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t own = smem_u32(red + (i == 0 || j1 >= rows ? jj : j1) * 128 + 4 * lane);
+#pragma unroll
+        for (int sp = 0; sp < kSkMaxSplits; ++sp)
+          if (sp < sc.splits) w[i][sp] = ld_dsmem_f32x4(map_to_cta(own, sp));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int sp = 0; sp < kSkMaxSplits; ++sp)
+          if (sp < sc.splits) {
+            v[0] += w[i][sp].x; v[1] += w[i][sp].y; v[2] += w[i][sp].z; v[3] += w[i][sp].w;
+          }
+        const int j = i == 0 ? jj : j1;
+        if (j < rows) finish4<T>(p, m0 + j, int64_t(tile) * 128 + 4 * lane, v);
+      }
+    }
+  }
+  cluster_sync();  // no CTA leaves its buffer while another may read it
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
