@@ -334,6 +334,15 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
         if (c0 + c < rows) red[(c0 + c) * 128 + 32 * q + lane] = __uint_as_float(u[c]);
     }
   }
+  // TMEM goes back before any CTA waits for another: a CTA that held it at the
+  // cluster barrier could keep out, on its SM, one of another cluster, a peer of
+  // which in turn keeps out the CTA that it waits for (products of two streams).
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, sc.tcols);
+  }
   cluster_sync();  // every CTA's partials are in its shared memory
   if (warp >= 2 && run) {
 #pragma unroll 1
@@ -363,12 +372,6 @@ linear_q8_rows_kernel(const __grid_constant__ CUtensorMap tmW,
     }
   }
   cluster_sync();  // no CTA leaves its buffer while another may read it
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, sc.tcols);
-  }
 }
 
 // ---------------------------------------------------------------------------

@@ -69,3 +69,26 @@ def test_a_weight_made_between_products():
     m.check_device()
     for i, (a, b) in enumerate(zip(outs, want)):
         assert torch.equal(a, b), i
+
+
+def test_split_products_on_two_streams_at_once():
+    # wide row tiles of few k-blocks, split over clusters whose CTAs share SMs and their TMEM with
+    # the other stream's
+    m = q3()
+    sides = []
+    for i, (M, K, N) in enumerate(((128, 512, 4736), (125, 256, 9000))):
+        cfg = _cfg(K)
+        x = torch.randn(M, K, generator=_gen(60 + i)).to(torch.bfloat16).cuda()
+        _, q, s = m.add_rms_norm_q8(cfg, x, None)
+        lin = m.quantize_weight_q8(_weight(N, K, 62 + i).cuda())
+        sides.append((q, s, lin, m.linear_q8(q, s, lin)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(50):
+        for i, (q, s, lin, _) in enumerate(sides):
+            outs[i].append(m.linear_q8(q, s, lin, stream=streams[i]))
+    torch.cuda.synchronize()
+    m.check_device()
+    for (_, _, _, want), got in zip(sides, outs):
+        assert all(torch.equal(g, want) for g in got)
