@@ -530,11 +530,9 @@ linear_q8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
           if (++stage == S) { stage = 0; ph ^= 1; }
         }
       }
-      // all issued MMAs complete before either CTA releases its TMEM
       if (elect_one()) umma_commit_pair(drain, 0x3);
       __syncwarp();
     }
-    mbar_wait<true>(drain, 0, p.err, kWhereLinearQ8, nullptr);
   } else if (warp >= 6) {
     griddep_wait();
     // Scale words: the bytes of four k-blocks for each row of x (lane's rows
@@ -656,6 +654,11 @@ linear_q8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
       }
     }
   }
+  // All issued MMAs complete before either CTA releases its TMEM. Behind the
+  // other roles: warp 1 of the odd CTA has no loop, and a wait from the start
+  // would have the time limit of one step for the whole product.
+  __syncthreads();
+  if (warp == 1) mbar_wait<true>(drain, 0, p.err, kWhereLinearQ8, nullptr);
   tc_fence_before();
   cluster_sync();  // no CTA of the pair leaves while the other may touch its memory
   if (warp == 1) {
