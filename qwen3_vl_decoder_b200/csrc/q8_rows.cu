@@ -39,7 +39,9 @@ struct Raw8 {
 
 // 1 / sqrt(ss / width + eps) in two parts, ss the sum of the lanes' values (one
 // warp). The last two levels of the sum, the quotient and the root keep their
-// remainders: what is left is an error of a tenth of a unit in the last place.
+// remainders, to 2^-40 of the result; what is left is half the error of the sum
+// before: up to 13 roundings of 2^-24 (four squares and sums, the two halves of
+// a pair, five levels in a warp, three here), 25 in rows wider than 8192.
 __device__ __forceinline__ float2 inv_rms(float ss, float width, float eps) {
 #pragma unroll
   for (int o = 16; o > 2; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -64,8 +66,10 @@ __device__ __forceinline__ float2 inv_rms(float ss, float width, float eps) {
 }
 
 // v = h / rms * gain / scale was rounded onto the middle of two e4m3 steps:
-// the neighbour on the side on which it lay (one value in a million; below
-// 2^-6, where e4m3 has fewer bits, a middle keeps its rounding).
+// the neighbour on the side on which h * gain * (inv + inv_lo) lies (one value
+// in a million; below 2^-6, where e4m3 has fewer bits, a middle keeps its
+// rounding). Right where the row's sum is: rows with exact sums get the bytes of
+// 64-bit arithmetic, of others see below.
 __device__ __noinline__ float off_middle(float v, float h, float gain, float inv, float inv_lo,
                                          float s) {
   const double y = fabs(double(h) * double(gain) * (double(inv) + double(inv_lo)) * double(s));
@@ -86,10 +90,13 @@ __device__ __noinline__ float off_middle(float v, float h, float gain, float inv
 // Instructions come close behind memory, hence the packed arithmetic and the
 // branches for what only infinities need. One warp makes 1 / rms for the block.
 // Measured: bf16 with a delta 4096 x 2560 15.0 us, 8192 x 5120 55 (5.4 TB/s),
-// fp32 2129 x 5120 15.7; with an fp32 1 / rms made by every warp, which turned
-// about one e4m3 value in 10 million over, 14.7, 52, 14.4. Before that step a
-// block per row without look-ahead took 18.2, 75, 19.3, and a ring of bulk
-// copies instead of registers 18.9 at the first size.
+// fp32 2129 x 5120 15.7; with an fp32 1 / rms made by every warp 14.7, 52, 14.4.
+// Before that step a block per row without look-ahead took 18.2, 75, 19.3, and a
+// ring of bulk copies instead of registers 18.9 at the first size. Of 67 million
+// random values 4 to 22 in rows of up to 5120, and 0 to 9 in wider ones, got
+// another e4m3 value than from 64-bit arithmetic, 31 to 64 by fp32 operations
+// one after the other. The scale is that of the fp32 values: a maximum that
+// rounds onto 448 scales keeps the smaller one.
 // ---------------------------------------------------------------------------
 template <typename T, int NV, bool PRE, bool DELTA>
 __global__ void __maxnreg__(NV == 1 ? 48 : 64)
@@ -180,7 +187,8 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
           // f * inv * g rounded once: about one value in a million lies so
           // near a border of e4m3 that an error in the last place turns it
           // over, and rounding f * inv as well turned over two to three times
-          // as many. What lands on a border all the same goes to off_middle. A product of two bf16 is exact.
+          // as many. What lands on a border all the same goes to off_middle.
+          // A product of two bf16 is exact.
           if constexpr (sizeof(T) == 2) {
             const uint64_t fg = f2_mul(f[i][j], g[j]);
             f[i][j] = f2_fma(fg, inv2, f2_mul(fg, lo2));
