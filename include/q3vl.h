@@ -398,7 +398,9 @@ int q3vl_lm_head(const q3vl_config* cfg, const void* x, int32_t B, const void* f
  *   y = RMSNorm(h) * gain in fp32 (y = h when gain is NULL),
  *   q, scales = the 8-bit form of y.
  * x, delta: device [S, H] in cfg dtype; delta may be NULL.
- * gain:     device [H] in cfg dtype, or NULL to quantise h without a norm.
+ * gain:     device [H] in cfg dtype, or NULL to quantise h without a norm. A
+ *           bf16 gain of 2^64 or more in magnitude is the device error
+ *           Q3VL_ERANGE; the row's bytes in its column may then be NaN.
  * h:        device [S, H] out; may be x or delta. Not written when delta is
  *           NULL (it may then be NULL).
  * q:        device e4m3 [S, H] out, 16-byte aligned.

@@ -23,6 +23,7 @@ enum WhereTag : int32_t {
   kWhereDecodeProducer = 501, kWhereDecodeMma = 502, kWhereDecodeEpilogue = 503,
   kWhereDecodeRange = 504, kWhereDecodeAttn = 505,
   kWhereStoreQ8Range = 701, kWhereAttnQ8Range = 702, kWhereAttnQ8 = 703, kWhereLinearQ8 = 704,
+  kWhereNormQ8Gain = 705,
   // bounds checks of the debug build (-DQ3VL_DEBUG)
   kWhereDbgAttnStore = 601, kWhereDbgGemmScratch = 602, kWhereDbgGemmRowsq = 603,
   kWhereDbgPositions = 604, kWhereDbgTable = 605, kWhereDbgRowstat = 606,

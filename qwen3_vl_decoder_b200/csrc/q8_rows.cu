@@ -65,6 +65,20 @@ __device__ __forceinline__ float2 inv_rms(float ss, float width, float eps) {
   return make_float2(inv, il);
 }
 
+// Whether a bf16 gain is one of those (finite, 2^64 and more) whose product with
+// an element may leave fp32 where h / rms * gain does not; elements are below
+// 2^64 while the sum of squares is finite. They are refused: a power of two of
+// 1 / rms put in front of the product would take them in, for 3 to 7% of the time.
+__device__ __forceinline__ bool far_gain(const Raw8<__nv_bfloat16>& g) {
+  float v[8];
+  g.floats(v);
+  bool far = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) far |= fabsf(v[j]) >= 0x1p64f && fabsf(v[j]) < INFINITY;
+  return far;
+}
+__device__ __forceinline__ bool far_gain(const Raw8<float>&) { return false; }  // h / rms first
+
 // v = h / rms * gain / scale was rounded onto the middle of two e4m3 steps:
 // the neighbour on the side on which h * gain * (inv + inv_lo) lies (one value
 // in a million; below 2^-6, where e4m3 has fewer bits, a middle keeps its
@@ -101,7 +115,8 @@ __device__ __noinline__ float off_middle(float v, float h, float gain, float inv
 template <typename T, int NV, bool PRE, bool DELTA>
 __global__ void __maxnreg__(NV == 1 ? 48 : 64)
 add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t* q,
-                       uint8_t* scales, int64_t rows, int width, int nblk, float eps) {
+                       uint8_t* scales, int64_t rows, int width, int nblk, float eps,
+                       int32_t* err) {
   const int t = threadIdx.x, lane = t & 31;
   const int units = width / 8;
   __shared__ float s_ss[2][32];
@@ -123,6 +138,12 @@ add_rms_norm_q8_kernel(const T* x, const T* delta, const T* gain, T* h, uint8_t*
   };
   if (PRE) request(blockIdx.x, t);
   if (NV == 1) request_gain(t);
+  if (sizeof(T) == 2 && blockIdx.x == 0) {
+    for (int u = t; u < NV * int(blockDim.x); u += blockDim.x) {
+      if (NV > 1) request_gain(u);
+      if (far_gain(gn)) record_error(err, Q3VL_ERANGE, kWhereNormQ8Gain);
+    }
+  }
   int par = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
     uint64_t f[NV][4];  // two elements each: packed fp32 arithmetic
@@ -473,7 +494,7 @@ cudaError_t launch_norm_t(const void* x, const void* delta, int64_t S, const voi
     return launch_pdl_plain(kern, dim3(static_cast<unsigned>(blocks)), dim3(th), 0, st,
                             static_cast<const T*>(x), static_cast<const T*>(delta),
                             static_cast<const T*>(gain), static_cast<T*>(h), q, scales, S, width,
-                            nblk, eps);
+                            nblk, eps, device_error_ptr());
   };
   cudaError_t e;
   if (units <= 1024)
