@@ -55,13 +55,19 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current device and its current stream's handle, by the functions below torch.cuda's where this
+# torch has them (no Stream object is built: 3 us a call).
+_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+               (lambda index: torch.cuda.current_stream(index).cuda_stream))
+
+
 def _stream(stream=None):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
     if not torch.cuda.is_initialized():
         torch.cuda.init()
-    # the current device's current stream, without building a Stream object (3 us a call)
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    return ctypes.c_void_p(_raw_stream(_device()))
 
 
 def config(hidden, n_heads, n_kv_heads, intermediate, dtype="bf16", qkv_bias=False,
@@ -420,9 +426,6 @@ def _is(t, dtype, shape, index: int) -> bool:
     """Whether _arg would accept t on CUDA device `index`, at a fraction of its cost."""
     return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
             t.get_device() == index and t.is_contiguous())
-
-
-_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _run(t: torch.Tensor, index: int, stream, call, *args):
