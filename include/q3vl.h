@@ -405,13 +405,15 @@ int q3vl_lm_head(const q3vl_config* cfg, const void* x, int32_t B, const void* f
  *           NULL (it may then be NULL).
  * q:        device e4m3 [S, H] out, 16-byte aligned.
  * scales:   device E8M0 [S, ceil(H / 128)] out.
- * q and h overlap no input otherwise. H <= 32768. */
+ * q, scales and h overlap neither one another nor an input otherwise.
+ * H <= 32768. */
 int q3vl_add_rms_norm_q8(const q3vl_config* cfg, const void* x, const void* delta, int64_t S,
                          const void* gain, void* h, uint8_t* q, uint8_t* scales,
                          q3vl_stream stream);
 
 /* 8-bit form of a weight matrix w [N, K] (device, cfg dtype): wq e4m3 [N, K]
- * and ws E8M0 [ceil(N / 128), ceil(K / 128)]. K must be a multiple of 64. */
+ * and ws E8M0 [ceil(N / 128), ceil(K / 128)], which overlap neither w nor each
+ * other. K must be a multiple of 64. */
 int q3vl_quantize_weight_q8(const q3vl_config* cfg, const void* w, int64_t N, int64_t K,
                             uint8_t* wq, uint8_t* ws, q3vl_stream stream);
 
@@ -422,8 +424,8 @@ int q3vl_quantize_weight_q8(const q3vl_config* cfg, const void* w, int64_t N, in
  * wq, ws: device e4m3 [N, K] and E8M0 [ceil(N / 128), ceil(K / 128)].
  * resid:  device [M, N] of the output type, or NULL; may be out.
  * out:    device [M, N], bf16 or fp32 by out_dtype (enum q3vl_dtype).
- * K must be a multiple of 64; M, N >= 1. xq, wq, resid and out 16-byte
- * aligned. */
+ * out overlaps no input otherwise. K must be a multiple of 64; M, N >= 1. xq,
+ * wq, resid and out 16-byte aligned. */
 int q3vl_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
                    const uint8_t* ws, int64_t N, int64_t K, const void* resid, void* out,
                    int32_t out_dtype, q3vl_stream stream);
@@ -434,7 +436,8 @@ size_t q3vl_lm_head_q8_workspace_bytes(const q3vl_config* cfg, int32_t B);
 /* q3vl_lm_head with an 8-bit output weight: the normalised rows are quantised
  * (q3vl_add_rms_norm_q8) and multiplied by wq/ws (q3vl_linear_q8) into fp32
  * logits. x: device bf16 [B, H], 1 <= B <= 256; wq, ws: [vocab, H] as
- * q3vl_quantize_weight_q8 writes them. */
+ * q3vl_quantize_weight_q8 writes them. logits and the workspace overlap neither
+ * each other nor an input. */
 int q3vl_lm_head_q8(const q3vl_config* cfg, const void* x, int32_t B, const void* final_norm,
                     const uint8_t* wq, const uint8_t* ws, int64_t vocab, float* logits,
                     void* wsp, size_t wsp_bytes, q3vl_stream stream);
@@ -458,7 +461,8 @@ typedef struct q3vl_kv_cache_q8 {
  * larger of its scale and the new rows'; where that grew, its earlier rows are
  * rounded again to it. Rows behind the last appended one are left as they are.
  * k, v:   device bf16, T rows of nkv*hd with row stride `ld` elements (a
- *         multiple of 8): e.g. the k and v column ranges of a QKV buffer.
+ *         multiple of 8): e.g. the k and v column ranges of a QKV buffer. They
+ *         lie outside the cache.
  * starts: device int32 [B + 1], sequence b's rows are starts[b] ..
  *         starts[b + 1] - 1 of the T; or NULL: T = B, one row per sequence.
  * seq:    device int32 [B], distinct slots in [0, n_seq).
@@ -487,6 +491,7 @@ size_t q3vl_attention_q8_workspace_bytes(const q3vl_config* cfg, int32_t B, int6
  *      the device error Q3VL_ERANGE and gives a zero row.
  * o:   device bf16 [B, nh*hd] out, 16-byte aligned; may be q.
  * ws:  >= q3vl_attention_q8_workspace_bytes bytes, 256-byte aligned.
+ * o and ws overlap neither each other nor the cache, ws not q either.
  * 1 <= B <= 256, n_heads / n_kv_heads in {1, 2, 4, 8}. */
 int q3vl_attention_q8(const q3vl_config* cfg, const void* q, int32_t B,
                       const q3vl_kv_cache_q8* kv, const int32_t* seq, const int32_t* len, void* o,

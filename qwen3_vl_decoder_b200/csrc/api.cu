@@ -4,6 +4,7 @@
 // q3vl_device_status().
 #include <atomic>
 #include <exception>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -1124,12 +1125,33 @@ int q3vl_lm_head(const q3vl_config* cfg, const void* x, int32_t B, const void* f
 // ---------------------------------------------------------------------------
 // 8-bit serving
 // ---------------------------------------------------------------------------
-static int check_gap_free(const void* a, size_t an, const void* b, size_t bn, const char* what) {
-  const char* a0 = static_cast<const char*>(a);
-  const char* b0 = static_cast<const char*>(b);
-  if (a != nullptr && b != nullptr && a0 < b0 + bn && b0 < a0 + an)
-    return set_error(Q3VL_EINVAL, std::string(what) + " must not overlap an input");
+// A buffer of a call, for the checks that what it writes lies apart.
+struct Span {
+  const char* name;
+  const void* at;
+  size_t bytes;
+};
+
+// `out` against each of `others` (NULL buffers take up no place).
+static int check_apart(const Span& out, std::initializer_list<Span> others) {
+  const char* a = static_cast<const char*>(out.at);
+  for (const Span& o : others) {
+    const char* b = static_cast<const char*>(o.at);
+    if (a != nullptr && b != nullptr && a < b + o.bytes && b < a + out.bytes)
+      return set_error(Q3VL_EINVAL, std::string(out.name) + " must not overlap " + o.name);
+  }
   return Q3VL_OK;
+}
+
+static size_t q8_blocks(int64_t n) { return static_cast<size_t>((n + kQ8Block - 1) / kQ8Block); }
+
+// `out` against the four buffers of an 8-bit cache.
+static int check_apart_kv(const q3vl_config* cfg, const Span& out, const q3vl_kv_cache_q8* kv) {
+  const size_t rows = size_t(kv->n_seq) * kv->cap * kv_dim(*cfg);
+  const size_t scales = size_t(kv->n_seq) * q8_blocks(kv->cap) * cfg->n_kv_heads;
+  return check_apart(out, {{"kv cache k", kv->k, rows}, {"kv cache v", kv->v, rows},
+                           {"kv cache k_scale", kv->k_scale, scales},
+                           {"kv cache v_scale", kv->v_scale, scales}});
 }
 
 int q3vl_add_rms_norm_q8(const q3vl_config* cfg, const void* x, const void* delta, int64_t S,
@@ -1150,13 +1172,15 @@ int q3vl_add_rms_norm_q8(const q3vl_config* cfg, const void* x, const void* delt
     Q3VL_TRY(check_ptr(scales, "scales", false));
     // rows are read ahead of those written
     const size_t qb = size_t(S) * cfg->hidden, xb = qb * elem_bytes(*cfg);
-    Q3VL_TRY(check_gap_free(q, qb, x, xb, "q"));
-    if (delta != nullptr) {
-      Q3VL_TRY(check_gap_free(q, qb, delta, xb, "q"));
-      Q3VL_TRY(check_gap_free(q, qb, h, xb, "q"));
-      if (h != x) Q3VL_TRY(check_gap_free(h, xb, x, xb, "h (unless it is x)"));
-      if (h != delta) Q3VL_TRY(check_gap_free(h, xb, delta, xb, "h (unless it is delta)"));
-    }
+    const Span sx{"x", x, xb}, sd{"delta", delta, xb},
+        sg{"gain", gain, size_t(cfg->hidden) * elem_bytes(*cfg)},
+        sh{"h", delta != nullptr ? h : nullptr, xb}, sq{"q", q, qb},
+        ss{"scales", scales, size_t(S) * q8_blocks(cfg->hidden)};
+    Q3VL_TRY(check_apart(sq, {sx, sd, sg, sh}));
+    Q3VL_TRY(check_apart(ss, {sx, sd, sg, sh, sq}));
+    if (h != x) Q3VL_TRY(check_apart(sh, {sx}));
+    if (h != delta) Q3VL_TRY(check_apart(sh, {sd}));
+    Q3VL_TRY(check_apart(sh, {sg}));
     return cuda_check(launch_add_rms_norm_q8(*cfg, x, delta, S, gain, h, q, scales, ST(stream)),
                       "8-bit norm");
   });
@@ -1172,14 +1196,17 @@ int q3vl_quantize_weight_q8(const q3vl_config* cfg, const void* w, int64_t N, in
     Q3VL_TRY(check_ptr(w, "w"));
     Q3VL_TRY(check_ptr(wq, "wq"));
     Q3VL_TRY(check_ptr(ws, "ws", false));
+    const Span sw{"w", w, size_t(N) * K * elem_bytes(*cfg)}, sq{"wq", wq, size_t(N) * K};
+    Q3VL_TRY(check_apart(sq, {sw}));
+    Q3VL_TRY(check_apart({"ws", ws, q8_blocks(N) * q8_blocks(K)}, {sw, sq}));
     return cuda_check(launch_quantize_weight_q8(*cfg, w, N, K, wq, ws, ST(stream)),
                       "8-bit weight");
   });
 }
 
-static int linear_q8_impl(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
-                          const uint8_t* ws, int64_t N, int64_t K, const void* resid, void* out,
-                          int32_t out_dtype, q3vl_stream stream) {
+static int check_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
+                           const uint8_t* ws, int64_t N, int64_t K, const void* resid,
+                           const void* out, int32_t out_dtype) {
   if (M < 1 || M > (int64_t(1) << 30)) return set_error(Q3VL_EINVAL, "M must be in [1, 2^30]");
   if (N < 1 || N > (int64_t(1) << 30)) return set_error(Q3VL_EINVAL, "N must be in [1, 2^30]");
   if (K < 64 || K % 64 != 0 || K > (int64_t(1) << 22))
@@ -1192,20 +1219,21 @@ static int linear_q8_impl(const uint8_t* xq, const uint8_t* xs, int64_t M, const
   Q3VL_TRY(check_ptr(ws, "ws", false));
   Q3VL_TRY(check_ptr(out, "out"));
   if (resid != nullptr) Q3VL_TRY(check_ptr(resid, "resid"));
-  const size_t ob = size_t(M) * N * (out_dtype == Q3VL_DTYPE_BF16 ? 2 : 4);
-  Q3VL_TRY(check_gap_free(out, ob, xq, size_t(M) * K, "out"));
-  Q3VL_TRY(check_gap_free(out, ob, wq, size_t(N) * K, "out"));
-  if (resid != out) Q3VL_TRY(check_gap_free(out, ob, resid, ob, "out (unless it is resid)"));
-  return cuda_check(launch_linear_q8(xq, xs, M, wq, ws, N, K, resid, out,
-                                     out_dtype == Q3VL_DTYPE_BF16, ST(stream)),
-                    "8-bit product");
+  const Span so{"out", out, size_t(M) * N * (out_dtype == Q3VL_DTYPE_BF16 ? 2 : 4)};
+  Q3VL_TRY(check_apart(so, {{"xq", xq, size_t(M) * K}, {"xs", xs, size_t(M) * q8_blocks(K)},
+                            {"wq", wq, size_t(N) * K}, {"ws", ws, q8_blocks(N) * q8_blocks(K)}}));
+  if (resid != out) Q3VL_TRY(check_apart(so, {{"resid (unless it is out)", resid, so.bytes}}));
+  return Q3VL_OK;
 }
 
 int q3vl_linear_q8(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
                    const uint8_t* ws, int64_t N, int64_t K, const void* resid, void* out,
                    int32_t out_dtype, q3vl_stream stream) {
   return no_throw([&]() -> int {
-    return linear_q8_impl(xq, xs, M, wq, ws, N, K, resid, out, out_dtype, stream);
+    Q3VL_TRY(check_linear_q8(xq, xs, M, wq, ws, N, K, resid, out, out_dtype));
+    return cuda_check(launch_linear_q8(xq, xs, M, wq, ws, N, K, resid, out,
+                                       out_dtype == Q3VL_DTYPE_BF16, ST(stream)),
+                      "8-bit product");
   });
 }
 
@@ -1235,10 +1263,18 @@ int q3vl_lm_head_q8(const q3vl_config* cfg, const void* x, int32_t B, const void
                                             std::to_string(need) + " bytes, 256-byte aligned");
     uint8_t* q = static_cast<uint8_t*>(wsp);
     uint8_t* s = q + align256(size_t(B) * cfg->hidden);
+    Q3VL_TRY(check_linear_q8(q, s, B, wq, ws, vocab, cfg->hidden, nullptr, logits,
+                             Q3VL_DTYPE_FP32));
+    const Span sx{"x", x, size_t(B) * cfg->hidden * 2},
+        sn{"final_norm", final_norm, size_t(cfg->hidden) * 2}, sp{"the workspace", wsp, need};
+    Q3VL_TRY(check_apart(sp, {sx, sn, {"wq", wq, size_t(vocab) * cfg->hidden},
+                              {"ws", ws, q8_blocks(vocab) * q8_blocks(cfg->hidden)}}));
+    Q3VL_TRY(check_apart({"logits", logits, size_t(B) * vocab * 4}, {sx, sn, sp}));
     Q3VL_CUDA(launch_add_rms_norm_q8(*cfg, x, nullptr, B, final_norm, nullptr, q, s, ST(stream)),
               "8-bit lm head norm");
-    return linear_q8_impl(q, s, B, wq, ws, vocab, cfg->hidden, nullptr, logits, Q3VL_DTYPE_FP32,
-                          stream);
+    return cuda_check(launch_linear_q8(q, s, B, wq, ws, vocab, cfg->hidden, nullptr, logits, false,
+                                       ST(stream)),
+                      "8-bit lm head product");
   });
 }
 
@@ -1272,6 +1308,9 @@ int q3vl_kv_store_q8(const q3vl_config* cfg, const void* k, const void* v, int64
     Q3VL_TRY(check_kv_q8(kv, "kv"));
     Q3VL_TRY(check_ptr(seq, "seq", false));
     Q3VL_TRY(check_ptr(len, "len", false));
+    const size_t rows = (size_t(T - 1) * ld + kv_dim(*cfg)) * 2;
+    Q3VL_TRY(check_apart_kv(cfg, {"k", k, rows}, kv));
+    Q3VL_TRY(check_apart_kv(cfg, {"v", v, rows}, kv));
     return cuda_check(launch_kv_store_q8(*cfg, k, v, ld, T, starts, B, *kv, seq, len, 0,
                                          ST(stream)),
                       "8-bit kv cache store");
@@ -1297,13 +1336,18 @@ int q3vl_attention_q8(const q3vl_config* cfg, const void* q, int32_t B,
     Q3VL_TRY(check_ptr(seq, "seq", false));
     Q3VL_TRY(check_ptr(len, "len", false));
     Q3VL_TRY(check_ptr(o, "o"));
-    const size_t ob = size_t(B) * q_dim(*cfg) * 2;
-    if (o != q) Q3VL_TRY(check_gap_free(o, ob, q, ob, "o (unless it is q)"));
+    const Span so{"o", o, size_t(B) * q_dim(*cfg) * 2};
+    if (o != q) Q3VL_TRY(check_apart(so, {{"q (unless it is o)", q, so.bytes}}));
     const size_t need = attention_q8_ws_bytes(*cfg, B, kv->cap);
     if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) != 0 || ws_bytes < need)
       return set_error(Q3VL_EWORKSPACE, "8-bit attention workspace too small: need " +
                                             std::to_string(need) + " bytes, 256-byte aligned");
-    return cuda_check(launch_attention_q8(*cfg, q, B, *kv, seq, len, nullptr, nullptr, o, ws, ST(stream)),
+    const Span sw{"the workspace", ws, need};
+    Q3VL_TRY(check_apart(sw, {so, {"q", q, so.bytes}}));
+    Q3VL_TRY(check_apart_kv(cfg, so, kv));
+    Q3VL_TRY(check_apart_kv(cfg, sw, kv));
+    return cuda_check(launch_attention_q8(*cfg, q, B, *kv, seq, len, nullptr, nullptr, o, ws,
+                                          ST(stream)),
                       "8-bit attention");
   });
 }
