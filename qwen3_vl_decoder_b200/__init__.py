@@ -244,6 +244,9 @@ class KvCacheQ8:
         return kv
 
     def _set(self, cfg, k, v, k_scale, v_scale):
+        _arg(k, "k", (torch.float8_e4m3fn,))
+        if k.dim() != 3:
+            raise Q3VLError(_abi.EINVAL, f"k must be [n_seq, cap, nkv*128], not {tuple(k.shape)}")
         n_seq, cap, dkv = k.shape
         blocks = -(-cap // Q8_BLOCK)
         for t, name in ((k, "k"), (v, "v")):
@@ -583,9 +586,10 @@ def _linear_q8(xq, scales, lin, resid, out_dtype, out, M, N, K, st):
 
 def _lm_head_q8(cfg, x_rows, final_norm, lin, logits, ws, stream):
     _arg(x_rows, "x_rows", (torch.bfloat16,))
-    B, (vocab, K) = x_rows.shape[0], lin.shape
+    vocab, K = lin.shape
     if x_rows.dim() != 2 or x_rows.shape[1] != cfg.hidden or K != cfg.hidden:
         raise Q3VLError(_abi.EINVAL, f"x_rows and weight must have {cfg.hidden} columns")
+    B = x_rows.shape[0]
     if final_norm is not None:
         _arg(final_norm, "final_norm", (torch.bfloat16,), (cfg.hidden,), x_rows.device)
     if lin.weight.device != x_rows.device:
@@ -626,9 +630,12 @@ def kv_store_q8(cfg: Config, k: torch.Tensor, v: torch.Tensor, kv: KvCacheQ8, se
     """
     if not isinstance(kv, KvCacheQ8):
         raise Q3VLError(_abi.EINVAL, "kv must be a KvCacheQ8")
+    if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and
+            isinstance(seq, torch.Tensor)):
+        raise Q3VLError(_abi.EINVAL, "k, v and seq must be tensors")
     dkv, index = cfg.n_kv_heads * cfg.head_dim, kv._index
     shape, strides = k.shape, k.stride()
-    T, B = shape[0], seq.numel()
+    T, B = shape[0] if shape else 0, seq.numel()
     # rows of dkv elements, one shape, type, stride and device
     if not (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and
             len(shape) == 2 and shape[1] == dkv and v.shape == shape and strides[1] == 1 and
