@@ -403,6 +403,7 @@ struct PairCfg {
   static constexpr size_t kSmem =
       1024 + size_t(kStages) * (kABytes + kBBytes) + size_t(kSlots) * kScales + kEpi + 256;
   static_assert(BN % 32 == 0 && kBBytes % 1024 == 0, "MMA and swizzle");
+  static_assert(BN > 128 && BN <= 256, "scale words of two times 128 weight rows");
   static_assert(kSfCol + 24 <= 512, "TMEM columns");
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -516,7 +517,7 @@ linear_q8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
             if (fresh) {
               tmem_cp_scales_pair(sfx, ds);
               tmem_cp_scales_pair(sfw, ds + kScaleBytes / 16);
-              if (BN > 128) tmem_cp_scales_pair(sfw + 4, ds + 2 * (kScaleBytes / 16));
+              tmem_cp_scales_pair(sfw + 4, ds + 2 * (kScaleBytes / 16));
               umma_commit_pair(sempty + slot, 0x3);
             }
 #pragma unroll
@@ -585,8 +586,7 @@ linear_q8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
         u[j] = b == 0 ? w[0] : b == 1 ? w[1] : w[2];
       }
       *reinterpret_cast<uint4*>(dst + kScaleBytes) = make_uint4(u[0], u[1], u[2], u[3]);
-      if (BN > 128)
-        *reinterpret_cast<uint4*>(dst + 2 * kScaleBytes) = make_uint4(u[4], u[5], u[6], u[7]);
+      *reinterpret_cast<uint4*>(dst + 2 * kScaleBytes) = make_uint4(u[4], u[5], u[6], u[7]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_peer(map_to_cta(smem_u32(sfull + slot), 0));
