@@ -418,7 +418,8 @@ int q3vl_quantize_weight_q8(const q3vl_config* cfg, const void* w, int64_t N, in
                             uint8_t* wq, uint8_t* ws, q3vl_stream stream);
 
 /* out[m][n] = sum_k x[m][k] w[n][k] (+ resid[m][n]) of 8-bit operands, summed
- * in fp32 and rounded once to the output type.
+ * in fp32 by the tensor core (off by at most 2 K 2^-24 of the sum of the
+ * magnitudes) and rounded once to the output type.
  * xq, xs: device e4m3 [M, K] and E8M0 [M, ceil(K / 128)] (as
  *         q3vl_add_rms_norm_q8 writes them).
  * wq, ws: device e4m3 [N, K] and E8M0 [ceil(N / 128), ceil(K / 128)].
@@ -481,7 +482,8 @@ size_t q3vl_attention_q8_workspace_bytes(const q3vl_config* cfg, int32_t B, int6
 /* Attention of one query row per sequence over the 8-bit cache: query head h
  * of row b over rows 0 .. len[b] - 1 of KV head h / (nh/nkv) in slot seq[b],
  * scale 1/sqrt(hd). len[b] = 0 gives a zero row.
- * Scores, maxima and sums are fp32. A probability is held to 2^-9 of itself,
+ * Scores, maxima and sums are fp32; q is exact down to 2^-18 of its head's
+ * largest element. A probability is held to 2^-9 of itself,
  * down to 2^-28 of the largest among the up to 64 rows that share its scale
  * (32 of a block of 128, and the same 32 of the next block), below that to
  * 2^-37 of that largest one.

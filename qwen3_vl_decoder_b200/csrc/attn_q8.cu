@@ -38,7 +38,7 @@
 // order (and writes the rows of sequences without tokens). A single sequence is
 // balanced as it is: then the up to 16 parts of a head are one cluster, which
 // joins them over DSMEM and saves the second launch (512 tokens 6.1 us against
-// 7.3, 4096 tokens 9.4, now 8.7, against 10.5, 32768 tokens 20.4 against 22.8;
+// 7.3, 4096 tokens 9.4, now 8.9, against 10.5, 32768 tokens 20.4 against 22.8;
 // and 2.4 us of the host's time). Inside a
 // decode call, whose next kernel's weights are on their way meanwhile, the
 // clusters gave nothing.

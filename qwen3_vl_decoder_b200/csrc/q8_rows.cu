@@ -103,8 +103,8 @@ __device__ __noinline__ float off_middle(float v, float h, float gain, float inv
 // reduce this one; that wants 48 registers, for three quarters of the threads.
 // Instructions come close behind memory, hence the packed arithmetic and the
 // branches for what only infinities need. One warp makes 1 / rms for the block.
-// Measured: bf16 with a delta 4096 x 2560 15.0 us, 8192 x 5120 55 (5.4 TB/s),
-// fp32 2129 x 5120 15.7; with an fp32 1 / rms made by every warp 14.7, 52, 14.4.
+// Measured: bf16 with a delta 4096 x 2560 15.1 us, 8192 x 5120 55.7 (5.3 TB/s),
+// fp32 2129 x 5120 15.3; with an fp32 1 / rms made by every warp 14.7, 52, 14.4.
 // Before that step a block per row without look-ahead took 18.2, 75, 19.3, and a
 // ring of bulk copies instead of registers 18.9 at the first size. Of 67 million
 // random values 4 to 22 in rows of up to 5120, and 0 to 9 in wider ones, got
