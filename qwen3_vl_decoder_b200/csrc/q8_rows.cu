@@ -357,18 +357,20 @@ __global__ void __launch_bounds__(256, 4) kv_store_q8_kernel(StoreQ8Params p) {
   bool falls = false;
   if (t < p.B) {
     const int b = t;
-    int slot, len, s0, n;
+    int slot, len, s0;
+    int64_t rows;  // of two starts of any value
     if (p.seq == nullptr) {
-      slot = p.seq0; len = 0; s0 = 0; n = static_cast<int>(p.T);
+      slot = p.seq0; len = 0; s0 = 0; rows = p.T;
     } else {
       slot = p.seq[b];
       len = p.len[b];
       s0 = p.starts ? p.starts[b] : b;
-      n = (p.starts ? p.starts[b + 1] : b + 1) - s0;
+      rows = int64_t(p.starts ? p.starts[b + 1] : b + 1) - s0;
     }
-    falls = n < 0;
-    const bool ok = slot >= 0 && slot < p.n_seq && len >= 0 && n >= 0 && s0 >= 0 &&
-                    int64_t(s0) + n <= p.T && int64_t(len) + n <= p.cap;
+    falls = rows < 0;
+    const bool ok = slot >= 0 && slot < p.n_seq && len >= 0 && rows >= 0 && s0 >= 0 &&
+                    s0 + rows <= p.T && len + rows <= p.cap;
+    const int n = ok ? static_cast<int>(rows) : 0;
     if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
       record_error(p.err, Q3VL_ERANGE, kWhereStoreQ8Range);
     const int64_t base = p.starts ? int64_t(s0) / 128 + 2 * b : b;
