@@ -507,8 +507,8 @@ def add_rms_norm_q8(cfg: Config, x: torch.Tensor, gain: Optional[torch.Tensor],
     """(h, q, scales): h = x + delta (x itself without a delta), and the 8-bit form of
     RMSNorm(h) * gain: e4m3 [S, H] with E8M0 scales [S, ceil(H/128)].
 
-    gain None quantises h without a norm. h: where to write the sum (x for in place); a new
-    tensor by default.
+    gain None quantises h without a norm; a bf16 gain of 2^64 or more is a device error. h: where
+    to write the sum (x for in place); a new tensor by default.
     """
     dt = torch_dtype(cfg)
     if not (isinstance(x, torch.Tensor) and x.dtype is dt and x.is_contiguous()):
